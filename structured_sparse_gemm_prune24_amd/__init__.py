@@ -16,6 +16,7 @@ not been built this module raises on first use -- there is no fallback.
     Y = p24.spmm_tw(w, X)
     c = p24.refresh(W); p24.mask_apply(W, c)   # masked fine-tuning
     b = p24.bw_compress(W, 16); e = p24.ew_compress(W, W.numel() // 4)   # comparison patterns
+    f = p24.compress_f8(W)              # 8-bit values; rms_norm, gated_act, spmm24_f8: see f8.py
 """
 from __future__ import annotations
 
@@ -29,6 +30,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 # that build.py --sanitize writes, for CPU test runs)
 LIB_PATH = os.environ.get("P24_LIBRARY") or os.path.join(PKG_DIR, "libprune24.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24.h")
+F8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24_f8.h")
 
 # status codes / enums (mirror include/prune24.h)
 P24_OK = 0
@@ -111,6 +113,19 @@ _SIGNATURES = {
     "gemm_bf16_pack": (_c_i32, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp]),
     "gemm_bf16": (_c_i32, [_c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i32, _c_i64, _c_vp]),
 }
+# entry points declared in include/prune24_f8.h
+_F8_SIGNATURES = {
+    "rms_norm": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_vp, _c_i64, _c_vp, ctypes.c_float, _c_i64, _c_i64, _c_vp, _c_i64,
+                          _c_vp, _c_i32, _c_i64, _c_vp, _c_vp]),
+    "gated_act": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_vp, _c_i64, _c_i32, _c_i64, _c_i64, _c_vp, _c_i32, _c_i64, _c_vp,
+                           _c_vp]),
+    "prune24_f8_bytes": (_c_size, [_c_i64, _c_i64]),
+    "prune24_compress_f8": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "prune24_decompress_f8": (_c_i32, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp]),
+    "spmm24_f8_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "spmm24_f8": (_c_i32, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i32, _c_i64, _c_vp,
+                           _c_i32, _c_vp, _c_i64, _c_vp, _c_size, _c_vp]),
+}
 
 _LIB = None
 
@@ -136,7 +151,7 @@ def lib() -> ctypes.CDLL:
         except ImportError:
             pass
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **_F8_SIGNATURES}.items():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
@@ -144,9 +159,9 @@ def lib() -> ctypes.CDLL:
     return _LIB
 
 
-def header_symbols() -> list[str]:
-    """Entry points declared with P24_API in include/prune24.h."""
-    with open(HEADER_PATH) as f:
+def header_symbols(path: str = HEADER_PATH) -> list[str]:
+    """Entry points declared with P24_API in a header, include/prune24.h unless another is named."""
+    with open(path) as f:
         text = f.read()
     return re.findall(r"P24_API\s+[\w\s\*]+?\b(\w+)\s*\(", text)
 
@@ -791,3 +806,17 @@ def gemm_bf16_xt(Wp, M: int, K: int, XT, out_dtype=None, out=None):
     _check(lib().gemm_bf16_xt(_ptr(Wp), M, K, _ptr(XT), ldxt, N, _ptr(out), _out_code(out.dtype), ldy,
                               _stream(XT.device)), "gemm_bf16_xt")
     return out
+
+
+# the 8-bit feed-forward operators need torch for their dtypes; the rest of the package imports it on use
+_F8_NAMES = ("Quantized8", "Compressed24F8", "rms_norm", "gated_act", "compress_f8", "decompress_f8", "spmm24_f8",
+             "feed_forward_f8")
+
+
+def __getattr__(name):
+    if name in _F8_NAMES:
+        from . import f8
+        value = getattr(f8, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,88 @@
+// Device-side building blocks of the 8-bit feed-forward operators (gfx950 only).
+#pragma once
+
+#include "p24_device.hpp"
+#include "../../include/prune24_f8.h"
+
+namespace p24 {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr float F8_MAX = 448.0f;
+constexpr float F32_TINY = 1.17549435e-38f;   // 2^-126
+
+// The layout of compressed 8-bit weights (include/prune24_f8.h).
+constexpr int F8_PIECE = 5120;                // one row group's 64-k block: 4 x 1 KiB values, 4 x 256 B positions
+__host__ __device__ inline int64_t f8_groups(int64_t M) { return (M + 127) / 128; }
+__host__ __device__ inline int64_t f8_steps(int64_t K) { return 2 * ((K + 127) / 128); }
+
+// Vectors loaded and stored at any element alignment: rows of an odd leading
+// dimension start anywhere, and global memory takes such accesses whole.
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+
+// Row storage types: fp32, bf16 bits, e4m3 bits.
+struct f8_t {
+  uint8_t v;
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// two fp32 -> packed bf16, round to nearest even
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+// four fp32 -> packed e4m3, round to nearest even; |v| <= 448 up to rounding, or NaN
+__device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+
+// NaN-propagating magnitude maximum: on the bits with the sign cleared NaN
+// ranks above infinity.
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Row scale of a magnitude maximum (NaN stays NaN).
+__device__ __forceinline__ float f8_scale(float amax) {
+  const float s = amax / F8_MAX;
+  return s < F32_TINY ? F32_TINY : s;
+}
+
+// GELU z/2 erfc(-z / sqrt 2) in fp32.  With x = |z| / sqrt 2 and
+// erfc(x) = erfcx(x) exp(-x^2), the smooth factor erfcx is t Q(t) with
+// t = 1 / (1 + 0.45 x) and Q of degree 9, a least-squares fit at Chebyshev nodes
+// reweighted to an even relative error of 3.3e-8; the negative side has no
+// cancellation.
+__device__ __forceinline__ float gelu_erfc(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.45f, x, 1.0f));
+  float q = fmaf(-0.04139154464337997f, t, 0.19068972595765202f);
+  q = fmaf(q, t, -0.30058562219818935f);
+  q = fmaf(q, t, 0.14240379306905548f);
+  q = fmaf(q, t, -0.022359379154972554f);
+  q = fmaf(q, t, 0.1199508486454104f);
+  q = fmaf(q, t, 0.1752520625005072f);
+  q = fmaf(q, t, 0.22827164669638228f);
+  q = fmaf(q, t, 0.25388316269317523f);
+  q = fmaf(q, t, 0.253885320751271f);
+  q *= t * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+  return 0.5f * z * (z >= 0.0f ? 2.0f - q : q);
+}
+
+// The activations of the 8-bit operators.  -inf gives NaN under SiLU and GELU
+// (infinity times zero), as their formulas do.
+__device__ __forceinline__ float f8_act(float z, int act) {
+  if (act == P24_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+  if (act == P24_ACT_GELU) return gelu_erfc(z);
+  if (act == P24_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays NaN
+  return z;
+}
+
+static inline bool f8_act_known(int32_t act) {
+  return act == P24_ACT_NONE || act == P24_ACT_RELU || act == P24_ACT_GELU || act == P24_ACT_SILU;
+}
+
+}  // namespace p24

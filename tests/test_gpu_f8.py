@@ -1,0 +1,366 @@
+"""GPU parity of the 8-bit feed-forward operators against fp64 formulas: RMS norm, gated
+activation, 2:4 compression into 8-bit rows, and the 2:4 product with its epilogue.
+
+Tolerances count roundings (U = 2^-24 is half an fp32 step, relative).
+Norm: the sum h is rounded once (U), its squares and their sum lose at most 8 values a chunk, 8
+chunks a thread, 6 wave steps and 16 waves (94 U, half of that under the root), the root and the
+quotients 6 U, the two products 2 U: 64 U of |y|, and twice that where y goes over the scale.
+An 8-bit value is half an e4m3 step off: 2^-4 of itself, or 2^-10 (half the subnormal step) times
+the scale.
+Product: 8-bit products are exact in fp32; K / 2 of them are summed in fp32, each addition at most
+one step (2 U) of the largest partial sum, which sum |w x| bounds.  With a bf16 output the 8-bit
+matrix unit adds eight products at a time, seven of them cut to 2^-13 of the largest: another
+7 * 2^-13 of sum |w x| at most.  (On small whole numbers nothing is cut: those are exact.)"""
+import numpy as np
+import pytest
+
+from f8_ref import F8, HALF, TINY, U, act, act_error, compress as ref_compress, decompress, pack, row_scale, smfmac64_model
+from gpu_util import need_gpu, torch
+
+p24 = pytest.importorskip("structured_sparse_gemm_prune24_amd")
+pytestmark = pytest.mark.gpu
+D = torch.float64
+
+
+def _rows(seed, tokens, width, pad, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    full = torch.randn(tokens, width + pad, generator=g, device="cuda")
+    full[:, ::7] *= 8
+    return full.to(dtype)[:, :width]
+
+
+def _check_rows(got, y, rel, out):
+    """got against fp64 y with relative error `rel` (a tensor or number) before the last rounding."""
+    if out == F8:
+        s = row_scale(y)
+        worst = float(rel.max()) if torch.is_tensor(rel) else rel
+        assert torch.all((got.scale.to(D) - s).abs() <= (worst + 4 * U) * s)
+        v = got.values.to(D) * got.scale.to(D)[:, None]
+        tol = (HALF[F8] + 2 * rel + 2 * worst + 8 * U) * y.abs() + 2.0 ** -10 * (1 + 2 * worst + 8 * U) * s[:, None]
+        assert got.values.to(torch.float32).abs().max() <= 448
+    else:
+        v = got.to(D)
+        assert got.dtype == out
+        tol = (HALF[out] + rel * (1 + HALF[out])) * y.abs() + 1e-36     # fp32 subnormals may flush
+    off = (v - y).abs()
+    assert torch.all(off <= tol), float((off / tol.clamp_min(1e-300)).max())
+
+
+NORM_SHAPES = [(1, 1, 0), (1, 64, 0), (3, 7, 2), (5, 511, 1), (4, 512, 0), (2, 513, 3), (7, 1003, 5), (2, 2048, 0),
+               (3, 2049, 7), (1, 4096, 0), (9, 4097, 0), (2, 8192, 8), (2, 8193, 0), (1, 16385, 1), (2, 40001, 3),
+               (1, 65536, 0), (300, 128, 0), (1025, 260, 4)]
+
+
+@pytest.mark.parametrize("out", [F8, torch.bfloat16, torch.float32], ids=["f8", "bf16", "f32"])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32], ids=["xbf16", "xf32"])
+@pytest.mark.parametrize("tokens,width,pad", NORM_SHAPES)
+def test_norm(tokens, width, pad, stream, out):
+    need_gpu()
+    w = 1 + 0.1 * _rows(9, 1, width, 0, torch.float32)[0]
+    for with_r in (False, True):
+        x = _rows(1, tokens, width, pad, stream)
+        r = _rows(2, tokens, width, pad + 1, stream) if with_r else None
+        y, h = p24.rms_norm(x, w, residual=r, out_dtype=out)
+        e = x.to(D) + r.to(D) if with_r else x.to(D)
+        if with_r:
+            assert h.dtype == stream
+            assert torch.all((h.to(D) - e).abs() <= (U + HALF[stream] * (1 + U)) * e.abs())
+        else:
+            assert h is None
+        e = e / torch.sqrt(e.square().mean(dim=1, keepdim=True) + 1e-6) * w.to(D)
+        _check_rows(y, e, 64 * U, out)
+
+
+@pytest.mark.parametrize("out", [F8, torch.bfloat16, torch.float32], ids=["f8", "bf16", "f32"])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32], ids=["xbf16", "xf32"])
+@pytest.mark.parametrize("name", ["silu", "gelu", "relu", "none"])
+@pytest.mark.parametrize("tokens,width,pad", [(1, 1, 0), (3, 7, 2), (4, 512, 0), (7, 1003, 5), (2, 4096, 8),
+                                              (2, 8193, 0), (4, 11264, 0), (1, 40001, 1), (777, 130, 0)])
+def test_gate(tokens, width, pad, name, stream, out):
+    need_gpu()
+    both = _rows(3, tokens, 2 * width, pad, stream)
+    for with_up in (True, False):
+        gate, up = both[:, :width], both[:, width:] if with_up else None
+        got = p24.gated_act(gate, up, act=name, out_dtype=out)
+        z = gate.to(D)
+        e = act(z, name)
+        rel = act_error(z, name) + U
+        if with_up:
+            e = e * up.to(D)
+        _check_rows(got, e, rel, out)
+
+
+@pytest.mark.parametrize("kind", ["zero", "nan", "inf", "tiny", "lowest"])
+def test_special_rows(kind):
+    """Rows of zeros, a NaN, an infinity, values under the smallest scale, the type's lowest value:
+    next to ordinary rows, which must not change."""
+    need_gpu()
+    x = _rows(5, 6, 700, 0, torch.float32)
+    clean = p24.gated_act(x, act="none")
+    bad = x.clone()
+    if kind == "zero":
+        bad[2] = 0
+    elif kind == "tiny":
+        bad[2] = 2.0 ** -130
+    else:
+        bad[2, 333] = {"nan": float("nan"), "inf": float("inf"), "lowest": torch.finfo(torch.float32).min}[kind]
+    got = p24.gated_act(bad, act="none")
+    y, _ = p24.rms_norm(bad, torch.ones(700, device="cuda"))
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(got.values.view(torch.uint8)[keep], clean.values.view(torch.uint8)[keep])
+    assert torch.equal(got.scale[keep], clean.scale[keep])
+    v, s = got.values.float()[2], got.scale[2].item()
+    vn, sn = y.values.float()[2], y.scale[2].item()
+    if kind == "zero":
+        assert s == sn == float(TINY) and not v.any() and not vn.any()
+    elif kind == "tiny":
+        assert s == float(TINY) and not torch.isnan(v).any()
+        assert torch.equal(v * 2.0 ** -126, torch.full_like(v, 2.0 ** -130))     # 2^-4 is an e4m3 value
+    elif kind == "nan":
+        assert np.isnan(s) and np.isnan(sn) and torch.isnan(v).all() and torch.isnan(vn).all()
+    elif kind == "inf":
+        assert np.isinf(s) and torch.isnan(v[333]) and not v[:333].any() and not v[334:].any()
+        assert np.isnan(sn)                          # inf / inf in the norm itself
+    else:
+        assert v[333] == -448 and np.isfinite(s)
+
+
+def test_norm_in_place_and_outputs():
+    need_gpu()
+    x, r = _rows(6, 33, 1000, 4, torch.bfloat16), _rows(7, 33, 1000, 0, torch.bfloat16)
+    w = torch.rand(1000, device="cuda")
+    y0, h0 = p24.rms_norm(x, w, residual=r)
+    for alias in ("x", "r"):
+        a, b = x.clone(), r.clone()
+        y, h = p24.rms_norm(a, w, residual=b, h=a if alias == "x" else b)
+        assert h is (a if alias == "x" else b)
+        assert torch.equal(h, h0) and torch.equal(y.values.view(torch.uint8), y0.values.view(torch.uint8))
+    big = p24.Quantized8(torch.zeros(33, 1100, dtype=torch.uint8, device="cuda").view(F8)[:, 50:1050],
+                         torch.zeros(33, device="cuda"))
+    y, _ = p24.rms_norm(x, w, residual=r, out=big)
+    assert y is big and torch.equal(big.scale, y0.scale)
+    whole = torch.as_strided(big.values.view(torch.uint8), (33, 1100), (1100, 1), 0)
+    assert torch.equal(whole[:, 50:1050], y0.values.view(torch.uint8))
+    assert not whole[:, :50].any() and not whole[:, 1050:].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,K", [(1, 64), (31, 64), (33, 192), (128, 128), (129, 320), (200, 1088)])
+def test_compress(M, K, dtype):
+    """Bit for bit: selection, ties, 8-bit values, positions, padding and scales."""
+    need_gpu()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M * K)
+    W = torch.randn(M, K + 3, generator=g, device="cuda").to(dtype)[:, :K]
+    W[:, ::5] = 0.5          # ties
+    W[0] = 0
+    c = p24.compress_f8(W)
+    bits, pos, scale = ref_compress(W.float().cpu().numpy())
+    assert np.array_equal(c.scale.cpu().numpy(), scale)
+    assert np.array_equal(c.data.cpu().numpy(), pack(bits, pos, M, K))
+    dense = p24.decompress_f8(c).cpu().numpy()
+    assert np.array_equal(dense, decompress(bits, pos, scale, K).astype(np.float32))
+
+
+def _weight(seed, M, K):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return p24.compress_f8(0.02 * torch.randn(M, K, generator=g, device="cuda"))
+
+
+def _product_ref(c, x, bias, name, r, out):
+    W = p24.decompress_f8(c).to(D)        # checked on its own above
+    X = x.values.to(D) * x.scale.to(D)[:, None]
+    z = X @ W.T
+    err = ((c.K + 16) * U + (7 * 2.0 ** -13 if out == torch.bfloat16 else 0)) * (X.abs() @ W.abs().T)
+    if bias is not None:
+        z = z + bias.to(D)
+        err = err + 2 * U * z.abs()
+    e = act(z, name)
+    err = 1.13 * err + act_error(z, name) * e.abs()      # no activation's slope passes 1.13
+    if r is not None:
+        e = e + r.to(D)
+        err = err + U * e.abs()
+    return e, err
+
+
+def _check_product(c, x, bias=None, name="none", r=None, out=torch.bfloat16, Y=None):
+    Y = p24.spmm24_f8(c, x, out_dtype=out, bias=bias, act=name, residual=r) if Y is None else Y
+    e, err = _product_ref(c, x, bias, name, r, out)
+    tol = err + HALF[out] * (e.abs() + err) + 1e-36
+    assert Y.dtype == out and tuple(Y.shape) == tuple(e.shape)
+    off = (Y.to(D) - e).abs()
+    assert torch.all(off <= tol), float((off / tol).max())
+    return Y
+
+
+SIZES = [(1, 32, 64), (1, 1, 64), (2, 33, 128), (1, 4096, 4096), (3, 100, 192), (24, 1000, 512), (31, 64, 64),
+         (32, 257, 320), (33, 129, 1088), (64, 512, 256), (65, 300, 128), (127, 96, 4032), (128, 128, 128),
+         (200, 640, 704), (257, 513, 64), (517, 1000, 448), (700, 2304, 768), (1000, 255, 2048), (2048, 1024, 320)]
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,M,K", SIZES)
+def test_product(N, M, K, out):
+    need_gpu()
+    c = _weight(M + K, M, K)
+    x = p24.gated_act(_rows(N, N, K, 0, torch.float32), act="none")
+    _check_product(c, x, out=out)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    bias = torch.randn(M, generator=g, device="cuda")
+    r = torch.randn(N, M + 3, generator=g, device="cuda").to(out)[:, :M]
+    for name in ("none", "relu", "gelu", "silu"):
+        _check_product(c, x, bias=bias, name=name, r=r if name != "relu" else None, out=out)
+    _check_product(c, x, r=r, out=out)
+
+
+@pytest.mark.parametrize("N,M,K", [(1, 64, 128), (5, 130, 4160), (40, 200, 192), (300, 300, 832), (600, 1500, 640)])
+def test_product_integers(N, M, K):
+    """Small whole numbers: every sum is exact in fp32, so the result is, whatever its order."""
+    need_gpu()
+    rng = np.random.default_rng(N)
+    W = rng.integers(-6, 7, (M, K)).astype(np.float32)
+    W[:, 0] = 7                                       # the row's largest: scale 7 / 448 = 2^-6
+    c = p24.compress_f8(torch.from_numpy(W).cuda())
+    q = torch.from_numpy(rng.integers(-4, 5, (N, K)).astype(np.float32)).cuda().to(F8)
+    x = p24.Quantized8(q, torch.full((N,), 2.0, device="cuda"))
+    dense = p24.decompress_f8(c)
+    assert torch.equal(dense * 64, (dense * 64).round())
+    want = (2 * q.to(D)) @ dense.to(D).T
+    for out in (torch.float32, torch.bfloat16):
+        assert torch.equal(p24.spmm24_f8(c, x, out_dtype=out), want.to(out))
+
+
+def test_product_does_not_read_past_its_rows():
+    """Tokens of a wider buffer whose other columns and rows are NaN, at every kernel's size."""
+    need_gpu()
+    for N, M, K in ((1, 96, 64), (20, 300, 192), (70, 300, 448), (300, 520, 320), (1000, 2048, 192)):
+        big = torch.full((N + 5, K + 64), 0x7F, dtype=torch.uint8, device="cuda").view(F8)     # NaN
+        src = p24.gated_act(_rows(N, N, K, 0, torch.float32), act="none")
+        big[:N, :K] = src.values
+        c = _weight(1, M, K)
+        Y = p24.spmm24_f8(c, p24.Quantized8(big[:N, :K], src.scale))
+        assert torch.equal(Y, p24.spmm24_f8(c, src))
+
+
+def test_product_of_a_nan_token():
+    """One token with a NaN scale: its row is NaN, the others keep their bits."""
+    need_gpu()
+    for N, M, K in ((3, 64, 128), (90, 300, 256), (500, 1024, 256)):
+        c = _weight(2, M, K)
+        x = p24.gated_act(_rows(N, N, K, 0, torch.float32), act="none")
+        Y0 = p24.spmm24_f8(c, x, out_dtype=torch.float32)
+        raw = _rows(N, N, K, 0, torch.float32).clone()
+        raw[1, 5] = float("nan")
+        Y = p24.spmm24_f8(c, p24.gated_act(raw, act="none"), out_dtype=torch.float32)
+        assert torch.isnan(Y[1]).all()
+        keep = [i for i in range(N) if i != 1]
+        assert torch.equal(Y[keep], Y0[keep])
+
+
+@pytest.mark.parametrize("N,M,K", [(1, 512, 256), (40, 300, 1024), (400, 1000, 320)])
+def test_product_in_place_on_the_residual(N, M, K):
+    need_gpu()
+    c = _weight(3, M, K)
+    x = p24.gated_act(_rows(4, N, K, 0, torch.float32), act="none")
+    r = _rows(5, N, M, 9, torch.bfloat16)
+    want = p24.spmm24_f8(c, x, residual=r, act="silu")
+    full = torch.zeros(N, M + 9, dtype=torch.bfloat16, device="cuda")
+    y = full[:, :M]
+    y.copy_(r)
+    got = p24.spmm24_f8(c, x, residual=y, out=y, act="silu")
+    assert got is y and torch.equal(y, want) and not full[:, M:].any()
+
+
+@pytest.mark.parametrize("N", [0, 1, 40, 600])
+def test_no_tokens_repeat_and_empty(N):
+    """Zero tokens are a no-op; the same call gives the same bits."""
+    need_gpu()
+    c = _weight(4, 300, 640)
+    x = p24.gated_act(_rows(4, N, 640, 0, torch.bfloat16), act="gelu")
+    a, b = p24.spmm24_f8(c, x), p24.spmm24_f8(c, x)
+    assert tuple(a.shape) == (N, 300) and torch.equal(a, b)
+    y, h = p24.rms_norm(_rows(1, N, 64, 0, torch.bfloat16), torch.ones(64, device="cuda"),
+                        residual=_rows(2, N, 64, 0, torch.bfloat16))
+    assert tuple(y.values.shape) == (N, 64) and tuple(h.shape) == (N, 64)
+
+
+def _layer(seed, tokens, width, f):
+    return (_rows(seed, tokens, width, 0, torch.bfloat16), _rows(seed + 1, tokens, width, 0, torch.bfloat16),
+            torch.rand(width, device="cuda") + 0.5, _weight(11, 2 * f, width), _weight(12, width, f))
+
+
+@pytest.mark.parametrize("tokens", [1, 24, 300])
+def test_feed_forward(tokens):
+    """The four calls together are the calls one by one, and near the layer in fp64 on the dequantized weights
+    (8-bit rows on the way: half an e4m3 step of each value, averaged over the sums)."""
+    need_gpu()
+    x, r, g, wgu, wd = _layer(20, tokens, 512, 704)
+    y, h = p24.feed_forward_f8(x, r, g, wgu, wd)
+    xq, h2 = p24.rms_norm(x, g, residual=r)
+    gu = p24.spmm24_f8(wgu, xq)
+    y2 = p24.spmm24_f8(wd, p24.gated_act(gu[:, :704], gu[:, 704:]), residual=h2)
+    assert torch.equal(h, h2) and torch.equal(y, y2)
+    e = x.to(D) + r.to(D)
+    n = e / torch.sqrt(e.square().mean(1, keepdim=True) + 1e-6) * g.to(D)
+    z = n @ p24.decompress_f8(wgu).to(D).T
+    a = act(z[:, :704], "silu") * z[:, 704:]
+    want = a @ p24.decompress_f8(wd).to(D).T
+    off = (y.to(D) - h.to(D)) - want
+    # relative to the layer's own output: two quantizations (each value within 2^-4) and bf16 between and after
+    assert off.norm() <= 0.15 * want.norm() + 2.0 ** -8 * h.to(D).norm()
+
+
+def test_graph_and_streams():
+    """One captured layer, replayed with eager work and new inputs in between, and a layer on a side stream."""
+    need_gpu()
+    x, r, g, wgu, wd = _layer(30, 40, 512, 704)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        p24.feed_forward_f8(x, r, g, wgu, wd)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = p24.feed_forward_f8(x, r, g, wgu, wd)
+    for k in range(4):
+        nx, nr = _rows(40 + k, 40, 512, 0, torch.bfloat16), _rows(50 + k, 40, 512, 0, torch.bfloat16)
+        ey, eh = p24.feed_forward_f8(nx, nr, g, wgu, wd)
+        x.copy_(nx)
+        r.copy_(nr)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ey) and torch.equal(h, eh), k
+    with torch.cuda.stream(side):
+        sy, _ = p24.feed_forward_f8(x, r, g, wgu, wd)
+    side.synchronize()
+    assert torch.equal(sy, y)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_smfmac_f8_lane_map(seed):
+    """One wavefront, one instruction, whole numbers: the hardware's lane map is the model's, exactly."""
+    need_gpu()
+    import ctypes
+    import os
+    p24.lib()
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "hw_probe", "libp24_smfmac_f8_probe.so")
+    if not os.path.exists(path):
+        pytest.fail(f"{path} is missing: build it with __graft_entry__.build()")
+    f = ctypes.CDLL(path).p24probe_smfmac64_f8
+    f.argtypes = [ctypes.c_void_p] * 5
+    rng = np.random.default_rng(seed)
+    a = rng.integers(-8, 9, (64, 16)).astype(np.float64)
+    b = rng.integers(-8, 9, (64, 32)).astype(np.float64)
+    nib = np.array([0x4, 0x8, 0xC, 0x9, 0xD, 0xE], dtype=np.uint32)[rng.integers(0, 6, (64, 8))]
+    words = np.zeros(64, dtype=np.uint32)
+    for q in range(8):
+        words |= nib[:, q] << np.uint32(4 * q)
+    ta, tb = (torch.from_numpy(v.astype(np.float32)).cuda().to(F8) for v in (a, b))
+    tw = torch.from_numpy(words.view(np.int32)).cuda()
+    d = torch.zeros(64, 16, device="cuda")
+    assert f(ta.data_ptr(), tb.data_ptr(), tw.data_ptr(), d.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert np.array_equal(d.cpu().numpy().astype(np.float64), smfmac64_model(a, b, words))
