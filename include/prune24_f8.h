@@ -110,8 +110,8 @@ P24_API p24_status prune24_decompress_f8(const void* data, const float* scale, i
  *               + residual[n][m]
  *   data, w_scale   the compressed M x K weight; K % 64 == 0, K > 0.
  *   X         N x K e4m3, leading dimension ldx >= K, ldx % 16 == 0, 16 B
- *             aligned, 512 * ldx < 2^32; N <= 65535 * 32, M < 2^24 (else
- *             P24_ERR_UNSUPPORTED).
+ *             aligned, 512 * ldx < 2^32; N <= 65535 * 32; M, K < 2^24
+ *             (else P24_ERR_UNSUPPORTED).
  *   x_scale   N fp32 values.
  *   Y         N x M, P24_F32 or P24_BF16 (round to nearest even), leading
  *             dimension ldy >= M, naturally aligned.
@@ -121,6 +121,10 @@ P24_API p24_status prune24_decompress_f8(const void* data, const float* scale, i
  *             pointer and leading dimension); otherwise Y overlaps no input.
  *   workspace device scratch, spmm24_f8_workspace_bytes(M, K, N) bytes, 16 B
  *             aligned, contents on entry do not matter; NULL where that is 0.
+ * The kernel is picked from the shape.  The environment variable
+ * P24_F8_TILE=tokens|64x32|64x64|128x64|128x128|256x128|256x256, read at each
+ * call, forces one (a measurement and test aid; results stay within the same
+ * bounds; 256x256 runs as 256x128 for a P24_F32 output).
  * Sums.  For a P24_F32 output every product is exact and every sum fp32.  For
  * a P24_BF16 output the 8-bit matrix unit adds eight products at a time, each
  * cut toward zero to 2^-13 of the exponent of the largest of the eight, and

@@ -1,7 +1,7 @@
 """Build libprune24.so (HIP for gfx950) in-tree, next to this file.
 
 Each .hip source is compiled to an object under <repo>/_build, then linked into
-the shared library.  Always recompiles (a build is the "does it build" check).
+the shared library; csrc/f8_call.cpp becomes _f8_call.so beside it.  Always recompiles (a build is the "does it build" check).
 The device assembly kept by -save-temps is checked by isa_check.
 
 `python build.py --sanitize` builds a second copy, _build/sanitize/libprune24.so,
@@ -119,11 +119,36 @@ def build_sanitized(verbose: bool = False) -> str:
     return out
 
 
+def build_call(verbose: bool = False) -> str:
+    """_f8_call.so, the C++ side of f8.py's calls: host code on PyTorch's C++ API, linked against
+    no copy of libprune24.so (it is given the entry points' addresses)."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    out = os.path.join(PKG, "_f8_call.so")
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", *(f for i in inc for f in ("-isystem", i)),
+           os.path.join(CSRC, "f8_call.cpp"), f"-L{os.path.join(torch, 'lib')}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_hip", "-ltorch_python", "-o", out + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: f8_call.cpp\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        call = ex.submit(build_call, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        call.result()
     out = os.path.join(PKG, LIB_NAME)
     tmp = out + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]

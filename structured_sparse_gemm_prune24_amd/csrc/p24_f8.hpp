@@ -72,13 +72,102 @@ __device__ __forceinline__ float gelu_erfc(float z) {
   return 0.5f * z * (z >= 0.0f ? 2.0f - q : q);
 }
 
-// The activations of the 8-bit operators.  -inf gives NaN under SiLU and GELU
-// (infinity times zero), as their formulas do.
-__device__ __forceinline__ float f8_act(float z, int act) {
-  if (act == P24_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
-  if (act == P24_ACT_GELU) return gelu_erfc(z);
-  if (act == P24_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays NaN
-  return z;
+// The activations of the 8-bit operators, over N values at a time: one uniform
+// branch, then straight code.  -inf gives NaN under SiLU and GELU (infinity times
+// zero), as their formulas do.
+__device__ __forceinline__ float silu_f32(float z) {
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+template <int N>
+__device__ __forceinline__ void f8_act(float (&z)[N], int act) {
+  if (act == P24_ACT_NONE) return;
+  if (act == P24_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = silu_f32(z[i]);
+  } else if (act == P24_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = gelu_erfc(z[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];   // NaN stays NaN
+  }
+}
+
+// Eight consecutive values from p, `left` of them inside the row.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
+  if (left >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      const u32x4 w = *reinterpret_cast<const u32x4_a2*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+      const u32x4 lo = *reinterpret_cast<const u32x4_a4*>(p), hi = *reinterpret_cast<const u32x4_a4*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(lo[i]);
+        v[4 + i] = __uint_as_float(hi[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.0f;
+      if (i < left) {
+        if constexpr (sizeof(T) == 2) v[i] = __uint_as_float((uint32_t)p[i] << 16);
+        else v[i] = p[i];
+      }
+    }
+  }
+}
+
+// NT: streamed past the L2, for outputs that are larger than it.
+template <bool NT>
+__device__ __forceinline__ void store_16b(void* p, u32x4 v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
+  else *reinterpret_cast<u32x4_a2*>(p) = v;
+}
+template <bool NT = false, typename T>
+__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 1) {
+    const uint32_t lo = pack_f8(v[0], v[1], v[2], v[3]), hi = pack_f8(v[4], v[5], v[6], v[7]);
+    if (left >= 8) {
+      *reinterpret_cast<u32x2_a1*>(p) = (u32x2){lo, hi};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) p[i].v = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    if (left >= 8) {
+      store_16b<NT>(p, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+  } else {
+    if (left >= 8) {
+      u32x4 lo, hi;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = __float_as_uint(v[i]);
+        hi[i] = __float_as_uint(v[4 + i]);
+      }
+      store_16b<NT>(p, lo);
+      store_16b<NT>(p + 4, hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  }
 }
 
 static inline bool f8_act_known(int32_t act) {

@@ -29,74 +29,6 @@ struct RowArgs {
   int act;
 };
 
-// Eight consecutive values from p, `left` of them inside the row.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
-  if (left >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const u32x4 w = *reinterpret_cast<const u32x4_a2*>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-      }
-    } else {
-      const u32x4 lo = *reinterpret_cast<const u32x4_a4*>(p), hi = *reinterpret_cast<const u32x4_a4*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(lo[i]);
-        v[4 + i] = __uint_as_float(hi[i]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (sizeof(T) == 2) v[i] = i < left ? __uint_as_float((uint32_t)p[i] << 16) : 0.0f;
-      else v[i] = i < left ? p[i] : 0.0f;
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
-  if constexpr (sizeof(T) == 1) {
-    const uint32_t lo = pack_f8(v[0], v[1], v[2], v[3]), hi = pack_f8(v[4], v[5], v[6], v[7]);
-    if (left >= 8) {
-      *reinterpret_cast<u32x2_a1*>(p) = (u32x2){lo, hi};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i].v = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
-    }
-  } else if constexpr (sizeof(T) == 2) {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    if (left >= 8) {
-      *reinterpret_cast<u32x4_a2*>(p) = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-    }
-  } else {
-    if (left >= 8) {
-      u32x4 lo, hi;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = __float_as_uint(v[i]);
-        hi[i] = __float_as_uint(v[4 + i]);
-      }
-      *reinterpret_cast<u32x4_a4*>(p) = lo;
-      *reinterpret_cast<u32x4_a4*>(p + 4) = hi;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = v[i];
-    }
-  }
-}
-
 // Sum and magnitude maximum over the G threads of a row, the same in each.
 template <int G>
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
@@ -157,15 +89,14 @@ __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
         for (int i = 0; i < 8; ++i) v[e][i] += u[i];
         store8((T*)args.h + row * args.ldh + c, width - c, v[e]);
       } else {
+        f8_act(v[e], args.act);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[e][i] = f8_act(v[e][i], args.act) * u[i];
+        for (int i = 0; i < 8; ++i) v[e][i] *= u[i];
       }
     }
   } else if constexpr (!NORM) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[e][i] = f8_act(v[e][i], args.act);
+    for (int e = 0; e < E; ++e) f8_act(v[e], args.act);
   }
   // values past the row are zero: act(0) = 0 for every activation
 #pragma unroll

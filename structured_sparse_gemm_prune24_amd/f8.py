@@ -13,6 +13,7 @@ rest of the binding this is argument marshalling only.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from dataclasses import dataclass
 
@@ -41,6 +42,26 @@ class Compressed24F8:
     scale: object        # torch.float32 [M]
     M: int
     K: int
+
+
+_CALL = None
+
+
+def _call():
+    """_f8_call.so: each call's checks, outputs and launch in one step where its arguments are of the
+    plain form, else None (csrc/f8_call.cpp); the code below then makes the call or names what is wrong."""
+    global _CALL
+    if _CALL is None:
+        L = lib()
+        try:
+            from . import _f8_call as c
+        except ImportError as e:
+            raise RuntimeError("_f8_call.so is missing: build it with __graft_entry__.build() "
+                               "or python structured_sparse_gemm_prune24_amd/build.py") from e
+        c.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.rms_norm, L.gated_act, L.spmm24_f8, L.spmm24_f8_workspace_bytes)))
+        _CALL = c
+    return _CALL
 
 
 def _rows(t, name, dev, dtypes, shape=None):
@@ -105,6 +126,11 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=F8, out=None, h=None)
     out_dtype torch.float8_e4m3fn (the default), else a bf16 or fp32 tensor; h has x's dtype, and
     is None without a residual.  `out` (a Quantized8 or tensor) and `h` give the outputs' place;
     h may be x or residual itself."""
+    if out is None and h is None and out_dtype in _CODES:
+        got = (_CALL or _call()).norm(x, weight, residual, eps, _CODES[out_dtype])
+        if got is not None:
+            y, s, h = got
+            return (y if s is None else Quantized8(y, s)), h
     dev = x.device
     ldx = _rows(x, "x", dev, _STREAM_TYPES)
     shape = tuple(x.shape)
@@ -136,6 +162,11 @@ def gated_act(gate, up=None, act="silu", out_dtype=F8, out=None):
     gate, up [tokens, width] fp32 or bf16, for instance the two halves of one product's output
     rows.  Returns a Quantized8 for out_dtype torch.float8_e4m3fn (the default), else a bf16 or
     fp32 tensor; `out` gives its place.  With act "none" and no `up` it quantizes the rows."""
+    if out is None and out_dtype in _CODES and act in _ACTS_F8:
+        got = (_CALL or _call()).gate(gate, up, _ACTS_F8[act], _CODES[out_dtype])
+        if got is not None:
+            y, s, _ = got
+            return y if s is None else Quantized8(y, s)
     dev = gate.device
     ldg = _rows(gate, "gate", dev, _STREAM_TYPES)
     shape = tuple(gate.shape)
@@ -182,6 +213,11 @@ def spmm24_f8(c: Compressed24F8, X: Quantized8, out_dtype=torch.bfloat16, out=No
     act "none", "relu", "gelu" or "silu"; residual [tokens, M] of the output's dtype, bf16 or
     fp32, and may be `out` itself."""
     v = X.values
+    if out is None and out_dtype in _STREAM_TYPES and act in _ACTS_F8:
+        Y = (_CALL or _call()).product(c.data, c.scale, c.M, c.K, v, X.scale, _CODES[out_dtype], bias, _ACTS_F8[act],
+                                       residual)
+        if Y is not None:
+            return Y
     dev = v.device
     ldx = _rows(v, "X.values", dev, (F8,))
     N, K = v.shape

@@ -20,7 +20,7 @@ from __future__ import annotations
 import re
 from typing import Dict, List, Tuple
 
-_KERNEL = re.compile(r"\n(_ZN3p246k_gemm\S+):[^\n]*\n(.*?)\.Lfunc_end", re.S)
+_KERNEL = re.compile(r"\n(_ZN3p24\d+k_gemm\S+):[^\n]*\n(.*?)\.Lfunc_end", re.S)
 _STORES = ("ds_write", "global_store", "buffer_store", "flat_store", "scratch_store")
 
 

@@ -216,6 +216,31 @@ def test_product(N, M, K, out):
     _check_product(c, x, r=r, out=out)
 
 
+TILES = ["tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x256"]
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,M,K", [(1, 1, 64), (33, 65, 128), (70, 300, 192), (129, 257, 448), (257, 260, 1024),
+                                   (100, 129, 1088), (300, 513, 1472), (64, 128, 4160)])
+@pytest.mark.parametrize("tile", TILES)
+def test_product_of_every_kernel(monkeypatch, tile, N, M, K, out):
+    """Each kernel at tokens, rows and K off its tile, K's parts within a block even and uneven; rows that the
+    tile reaches past the output stay untouched."""
+    need_gpu()
+    monkeypatch.setenv("P24_F8_TILE", tile)
+    c = _weight(M + K, M, K)
+    x = p24.gated_act(_rows(N, N, K, 0, torch.float32), act="none")
+    full = torch.full((N + 2, M + 5), 7.0, dtype=out, device="cuda")
+    y = full[1:N + 1, :M]
+    p24.spmm24_f8(c, x, out=y)
+    _check_product(c, x, out=out, Y=y)
+    assert (full[0] == 7).all() and (full[-1] == 7).all() and (full[:, M:] == 7).all()
+    r = _rows(5, N, M, 3, out)
+    bias = _rows(6, 1, M, 0, torch.float32)[0].contiguous()
+    for name in ("gelu", "silu"):
+        _check_product(c, x, bias=bias, name=name, r=r, out=out)
+
+
 @pytest.mark.parametrize("N,M,K", [(1, 64, 128), (5, 130, 4160), (40, 200, 192), (300, 300, 832), (600, 1500, 640)])
 def test_product_integers(N, M, K):
     """Small whole numbers: every sum is exact in fp32, so the result is, whatever its order."""
