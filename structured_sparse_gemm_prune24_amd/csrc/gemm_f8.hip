@@ -30,34 +30,8 @@ struct F8Args {
   int M, N, K;
   int act;
   int nbm, nbn;   // grid of block tiles
+  int res_dma;    // the residual is whole aligned 16 B chunks: it can go straight to LDS
 };
-
-// Four consecutive features m .. m+3 of token n from the fp32 sums: scales,
-// bias, activation, residual, one rounding.
-template <typename OutT>
-__device__ __forceinline__ void finish4(const F8Args& a, int n, int m, f32x4 sum) {
-  const float sx = a.x_scale[n];
-  OutT* y = (OutT*)a.Y + (int64_t)n * a.ldy + m;
-  const OutT* r = a.residual ? (const OutT*)a.residual + (int64_t)n * a.ldr + m : nullptr;
-  float z[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    z[i] = sum[i] * sx;
-    if (m + i < a.M) z[i] = fmaf(z[i], a.w_scale[m + i], a.bias ? a.bias[m + i] : 0.0f);
-  }
-  f8_act(z, a.act);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (m + i >= a.M) break;
-    if constexpr (sizeof(OutT) == 2) {
-      if (r) z[i] += __uint_as_float((uint32_t)r[i] << 16);
-      y[i] = (uint16_t)pack_bf16(z[i], 0.0f);
-    } else {
-      if (r) z[i] += r[i];
-      y[i] = z[i];
-    }
-  }
-}
 
 // Eight e4m3 values widened to bf16 (exact).
 __device__ __forceinline__ bf16x8 widen8(uint32_t v0, uint32_t v1) {
@@ -68,67 +42,117 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t v0, uint32_t v1) {
   return (bf16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// One 64-k block of a 32 x 32 tile.  On the bf16 unit instruction j takes stored
-// values 8 j .. 8 j + 7 of each lane, which are k 16 j + [0, 16) of lanes 0..31 and
-// 32 + 16 j + [0, 16) of lanes 32..63; its token operand is then, in lane L,
-// k 16 j + 8 (L / 32) + [0, 8) and the same 32 further on.  `x` points at the
-// block's first k of this lane's token.
+// One lane's operands of a 64-k block of a 32 x 32 tile, and their product.  On
+// the bf16 unit instruction j takes stored values 8 j .. 8 j + 7 of each lane, which
+// are k 16 j + [0, 16) of lanes 0..31 and 32 + 16 j + [0, 16) of lanes 32..63; its
+// token operand is then, in lane L, k 16 j + 8 (L / 32) + [0, 8) and the same 32
+// further on.
 template <bool EXACT>
-__device__ __forceinline__ f32x16 block_product(i32x4 a, int pos, const uint8_t* x, int half, f32x16 acc) {
-  if constexpr (EXACT) {
+struct F8Block {
+  i32x4 a;
+  int pos;
+  u32x4 x[2];
+  // `w` and `p`: this lane's values and positions, `xp`: the block's first k of this lane's token
+  __device__ __forceinline__ void load(const uint8_t* w, const uint8_t* p, const uint8_t* xp, int half) {
+    a = *reinterpret_cast<const i32x4*>(w);
+    pos = *reinterpret_cast<const int*>(p);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const u32x2 lo = *reinterpret_cast<const u32x2*>(x + 16 * j + 8 * half);
-      const u32x2 hi = *reinterpret_cast<const u32x2*>(x + 32 + 16 * j + 8 * half);
-      const bf16x16 b = __builtin_shufflevector(widen8(lo[0], lo[1]), widen8(hi[0], hi[1]), 0, 1, 2, 3, 4, 5, 6, 7, 8,
-                                                9, 10, 11, 12, 13, 14, 15);
-      const bf16x8 av = widen8((uint32_t)a[2 * j], (uint32_t)a[2 * j + 1]);
-      acc = j == 0 ? __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, b, acc, pos, 0, 0)
-                   : __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, b, acc, pos, 0, 1);
+    for (int q = 0; q < 2; ++q) {
+      if constexpr (EXACT) {
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(xp + 32 * q + 8 * half);
+        const u32x2 hi = *reinterpret_cast<const u32x2*>(xp + 32 * q + 16 + 8 * half);
+        x[q] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
+      } else {
+        x[q] = *reinterpret_cast<const u32x4*>(xp + 32 * q + 16 * half);
+      }
     }
-    return acc;
-  } else {
-    const i32x4 b0 = *reinterpret_cast<const i32x4*>(x + 16 * half);
-    const i32x4 b1 = *reinterpret_cast<const i32x4*>(x + 32 + 16 * half);
-    const i32x8 b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-    return __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(a, b, acc, pos, 0, 0);
   }
-}
+  __device__ __forceinline__ f32x16 product(f32x16 acc) const {
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bf16x16 b = __builtin_shufflevector(widen8(x[0][2 * j], x[0][2 * j + 1]),
+                                                  widen8(x[1][2 * j], x[1][2 * j + 1]), 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10,
+                                                  11, 12, 13, 14, 15);
+        const bf16x8 av = widen8((uint32_t)a[2 * j], (uint32_t)a[2 * j + 1]);
+        acc = j == 0 ? __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, b, acc, pos, 0, 0)
+                     : __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, b, acc, pos, 0, 1);
+      }
+      return acc;
+    } else {
+      const i32x8 b = __builtin_shufflevector(__builtin_bit_cast(i32x4, x[0]), __builtin_bit_cast(i32x4, x[1]), 0, 1, 2,
+                                              3, 4, 5, 6, 7);
+      return __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(a, b, acc, pos, 0, 0);
+    }
+  }
+};
 
 // A 32-row x 32-token tile per block; its W waves split K, every wave taking
-// 64-k blocks w, w + W, ..., and the partial tiles meet in LDS, summed in wave
-// order.  Nothing is shared between the waves before that, so each streams its
-// part of the weights at its own pace.
+// 64-k blocks w, w + W, ..., four of them on the way at a time, and the partial
+// tiles meet in LDS, summed in wave order.  Nothing is shared between the waves
+// before that, so each streams its part of the weights at its own pace.  With few
+// tokens the time is the launch and one trip to memory, so what the last part
+// needs (scales, bias, residual) is asked for first.
 template <int W, typename OutT>
 __global__ __launch_bounds__(W * 64) void k_f8_tokens(const F8Args args) {
+  constexpr bool EXACT = sizeof(OutT) == 4;
   constexpr int PITCH = 36;   // floats per token: 32 rows, padded so that the 16-byte writes spread over the banks
   __shared__ __attribute__((aligned(16))) float part[W][32 * PITCH];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
   const int rb = blockIdx.x;
   const int n0 = blockIdx.y * 32;
-  const int64_t steps = f8_steps(args.K);
-  const int n = min(n0 + (lane & 31), args.N - 1);
-  const uint8_t* x = args.X + n * args.ldx;
-  const uint8_t* group = args.W + (rb / 4) * steps * F8_PIECE;
-  const uint32_t v_off = (rb % 4) * 1024 + lane * 16, p_off = 4096 + (rb % 4) * 256 + lane * 4;
+  const int blocks = args.K / 64;
+  const uint8_t* x = args.X + (int64_t)min(n0 + (lane & 31), args.N - 1) * args.ldx;
+  const uint8_t* group = args.W + (rb / 4) * f8_steps(args.K) * F8_PIECE;
+  const uint8_t* w = group + (rb % 4) * 1024 + lane * 16;
+  const uint8_t* p = group + 4096 + (rb % 4) * 256 + lane * 4;
+
+  // the four features of a token that this thread finishes (the first 256 threads)
+  const int tn = threadIdx.x / 8, tm = (threadIdx.x % 8) * 4;
+  const int n = n0 + tn, m = rb * 32 + tm;
+  const bool finisher = tn < 32 && n < args.N && m < args.M;
+  float ws[4], bs[4] = {0, 0, 0, 0}, r[4] = {0, 0, 0, 0}, sx = 0.0f;
+  if (finisher) {
+    sx = args.x_scale[n];
+    load_row<4>(args.w_scale + m, args.M - m, ws);
+    if (args.bias) load_row<4>(args.bias + m, args.M - m, bs);
+    if (args.residual) load_row<4>((const OutT*)args.residual + (int64_t)n * args.ldr + m, args.M - m, r);
+  }
+
+  constexpr int U = 4;
   f32x16 acc = {};
-  for (int s = wave; s < args.K / 64; s += W) {
-    const uint8_t* piece = group + (int64_t)s * F8_PIECE;
-    const i32x4 a = *reinterpret_cast<const i32x4*>(piece + v_off);
-    const int pos = *reinterpret_cast<const int*>(piece + p_off);
-    acc = block_product<sizeof(OutT) == 4>(a, pos, x + (int64_t)s * 64, lane >> 5, acc);
+  int s = wave;
+  for (; s + (U - 1) * W < blocks; s += U * W) {
+    F8Block<EXACT> b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = s + u * W;
+      b[u].load(w + at * F8_PIECE, p + at * F8_PIECE, x + at * 64, half);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc = b[u].product(acc);
+  }
+  for (; s < blocks; s += W) {
+    F8Block<EXACT> b;
+    b.load(w + (int64_t)s * F8_PIECE, p + (int64_t)s * F8_PIECE, x + (int64_t)s * 64, half);
+    acc = b.product(acc);
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<f32x4*>(&part[wave][(lane & 31) * PITCH + 8 * q + 4 * (lane >> 5)]) =
+    *reinterpret_cast<f32x4*>(&part[wave][(lane & 31) * PITCH + 8 * q + 4 * half]) =
         (f32x4){acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
   __syncthreads();
-  for (int q = threadIdx.x; q < 256; q += W * 64) {
-    const int tn = q / 8, tm = (q % 8) * 4;
-    f32x4 z = {};
+  if (finisher) {
+    f32x4 sum = {};
 #pragma unroll
-    for (int w = 0; w < W; ++w) z += *reinterpret_cast<const f32x4*>(&part[w][tn * PITCH + tm]);
-    if (n0 + tn < args.N) finish4<OutT>(args, n0 + tn, rb * 32 + tm, z);
+    for (int v = 0; v < W; ++v) sum += *reinterpret_cast<const f32x4*>(&part[v][tn * PITCH + tm]);
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = fmaf(sum[i] * sx, ws[i], bs[i]);
+    f8_act(z, args.act);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] += r[i];
+    store_row<4>((OutT*)args.Y + (int64_t)n * args.ldy + m, args.M - m, z);
   }
 }
 
@@ -162,9 +186,18 @@ struct F8Tile {
   static_assert(BM % 128 == 0 || BM == 64 || BM == 32, "whole row groups, or an aligned part of one");
   static_assert(NSTAGE * KG * STAGE <= 160 * 1024, "LDS");
   static_assert(NSTAGE * DMA < 64, "vmcnt range");
-  // epilogue: each wave turns one 32-token slice at a time through LDS
+  // epilogue by slices (fp32 outputs, split K): each wave turns one 32-token slice at a time through LDS
   static constexpr int PITCH = WTM + 4;                    // floats per token
   static_assert(GWAVES * 32 * PITCH * 4 <= NSTAGE * STAGE, "the slices fit the stages' LDS");
+  // epilogue in place (bf16 outputs): each wave's output tile as bf16, RPS of them in a stage
+  static constexpr int REGION = WTM * WTN * 2, RL = REGION / 1024;   // bytes, and 1 KiB loads of its residual
+  static constexpr int RPS = STAGE / REGION < GWAVES ? STAGE / REGION : GWAVES;
+  static constexpr int RDMA = RPS * RL / LW;               // residual loads per loading wave and stage
+  static constexpr int CH = WTM / 8;                       // 16 B chunks per token of a region
+  static constexpr int X_SCALES = BN < 64 ? 64 : BN;
+  static constexpr int SCALES = (2 * BM + X_SCALES) * 4;   // weight scales, bias, token scales
+  static_assert(RPS >= 1 && (RPS * RL) % LW == 0 && RDMA <= DMA, "residual loads take the place of a step's loads");
+  static_assert((GWAVES + RPS - 1) / RPS <= NSTAGE, "the regions fit the stages");
 };
 
 template <int I, int N, typename F>
@@ -228,6 +261,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_rsrc(const uint8_t* base, u
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, soff, 0, 0);
 }
+// the same with 4 bytes per lane
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, voff, soff, 0, 0);
+}
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -237,10 +274,10 @@ __device__ __forceinline__ void wait_loads() {
 template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
 __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args args) {
   using C = F8Tile<BM, BN, WGM, WGN, LW, KG>;
-  constexpr bool EXACT = sizeof(OutT) == 4;
+  constexpr bool EXACT = sizeof(OutT) == 4, INPLACE = !EXACT && KG == 1;
   constexpr int TM = C::TM, TN = C::TN, NSTAGE = C::NSTAGE;
   typedef F8Frags<TM, TN, EXACT> Frags;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KG * NSTAGE * C::STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KG * NSTAGE * C::STAGE + (INPLACE ? C::SCALES : 0)];
 
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -309,6 +346,29 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     }
   };
 
+  // The residual of region r (wave r's output tile) on its way to LDS, in the
+  // stages that the last steps leave free: RPS regions a stage, the stage of
+  // "step" count + r / RPS.  A region is [token][16 B chunk c of its features] with
+  // chunk c of token t at place c ^ (t % CH): both the accumulators' order (one
+  // feature quad of 32 tokens) and whole rows then spread over the banks.
+  const __amdgpu_buffer_rsrc_t r_rsrc =
+      f8_rsrc((const uint8_t*)args.residual + ((int64_t)n0 * args.ldr + m0) * 2,
+              (uint32_t)(INPLACE && args.res_dma ? ((int64_t)(n_rows - 1) * args.ldr + args.M - m0) * 2 : 0));
+  const int r_t = lane / C::CH;                                  // token of a lane in its load, 64 / CH a load
+  auto issue_residual = [&](auto Q, int it, uint32_t st) {
+    constexpr int q = decltype(Q)::value;
+    const int l = q * LW + wave;                                 // load l of the stage, of its region l / RL
+    const int r = (it - count) * C::RPS + l / C::RL;
+    if (q < C::RDMA && r < C::GWAVES) {
+      const int t = (l % C::RL) * (64 / C::CH) + r_t;            // token of the region
+      const int chunk = (lane % C::CH) ^ (t % C::CH);
+      load_to_lds(r_rsrc, lds + st + l * 1024, (uint32_t)((t * args.ldr + 8 * chunk) * 2),
+                  (uint32_t)(((r % WGN) * C::WTN * args.ldr + (r / WGN) * C::WTM) * 2));
+    } else if (it == count || it < NSTAGE) {
+      issue(Q, it, st);     // until the last step has landed the waits count on a whole step's loads
+    }
+  };
+
   // LDS read addresses
   const int nl = lane & 31;
   const uint32_t b_row = (uint32_t)(wn * C::WTN + (nl ^ ((nl >> 3) & 1))) * 128;
@@ -354,7 +414,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   // The multiplies of one 64-k block, with the reads of the next one (block RSS
   // of the stage at byte rst) spread over their first three quarters and, where
   // LD, this wave's loads of step g into the stage at byte lst, one after each
-  // multiply.
+  // multiply (LD 1: operands, 2: the residual).
   auto block = [&](auto LD, const Frags& f, Frags& next, auto RSS, uint32_t rst, int g, uint32_t lst) {
     constexpr int NM = TM * TN, SPREAD = NM * 3 / 4 > 0 ? NM * 3 / 4 : 1;
     static_for<0, NM>([&](auto K) {
@@ -373,20 +433,40 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
         const i32x8 bv = __builtin_shufflevector(f.b[j][0], f.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
         acc[i][j] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(f.a[i], bv, acc[i][j], f.pos[i], 0, 0);
       }
-      if constexpr (decltype(LD)::value && k < C::DMA) issue(K, g, lst);
+      if constexpr (decltype(LD)::value == 1 && k < C::DMA) issue(K, g, lst);
+      if constexpr (decltype(LD)::value == 2 && k < C::DMA) issue_residual(K, g, lst);
       constexpr int lo = k < SPREAD ? NR * k / SPREAD : NR, hi = k < SPREAD ? NR * (k + 1) / SPREAD : NR;
       static_for<lo, hi>([&](auto R) { read_one(RSS, R, rst, next); });
       __builtin_amdgcn_sched_barrier(0);
     });
-    if constexpr (decltype(LD)::value)
-      static_for<NM < C::DMA ? NM : C::DMA, C::DMA>([&](auto Q) { issue(Q, g, lst); });
+    static_for<NM < C::DMA ? NM : C::DMA, C::DMA>([&](auto Q) {
+      if constexpr (decltype(LD)::value == 1) issue(Q, g, lst);
+      if constexpr (decltype(LD)::value == 2) issue_residual(Q, g, lst);
+    });
   };
 
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  const bool residual_dma = INPLACE && args.res_dma;
+  if constexpr (INPLACE) {
+    // scales and bias, 64 at a time, ahead of everything else
+    uint8_t* sc = lds_all + NSTAGE * C::STAGE;
+    const __amdgpu_buffer_rsrc_t ws = f8_rsrc((const uint8_t*)(args.w_scale + m0), (uint32_t)(args.M - m0) * 4);
+    const __amdgpu_buffer_rsrc_t bs =
+        f8_rsrc((const uint8_t*)(args.bias ? args.bias + m0 : nullptr), args.bias ? (uint32_t)(args.M - m0) * 4 : 0);
+    const __amdgpu_buffer_rsrc_t xs = f8_rsrc((const uint8_t*)(args.x_scale + n0), (uint32_t)n_rows * 4);
+    for (int u = wave; u < BM / 64; u += C::GWAVES) load4_to_lds(ws, sc + u * 256, lane * 4, u * 256);
+    if (args.bias)
+      for (int u = wave; u < BM / 64; u += C::GWAVES) load4_to_lds(bs, sc + BM * 4 + u * 256, lane * 4, u * 256);
+    for (int u = wave; u < C::X_SCALES / 64; u += C::GWAVES) load4_to_lds(xs, sc + BM * 8 + u * 256, lane * 4, u * 256);
+  }
 #pragma unroll
   for (int g = 0; g < NSTAGE; ++g)
-    if (loader) static_for<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE); });
+    if (loader) {
+      if (residual_dma && g >= count) static_for<0, C::DMA>([&](auto Q) { issue_residual(Q, g, g * C::STAGE); });
+      else static_for<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE); });
+    }
   wait_loads<(NSTAGE - 1) * C::DMA>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -398,10 +478,10 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   // blocks says that every wave has read the stage (its reads were waited for)
   // and that step it + 1 has landed (every loading wave waited for its part):
   // the stage is then refilled with step it + NSTAGE.  Steps past the end load
-  // the last one again, into stages that are not read.
+  // the last one again, or the residual, into stages that are not read.
   auto body = [&](auto LD, int it, uint32_t st) {
     const uint32_t nx = st == (NSTAGE - 1) * C::STAGE ? 0 : st + C::STAGE;
-    block(std::false_type{}, f0, f1, I1{}, st, 0, 0);
+    block(I0{}, f0, f1, I1{}, st, 0, 0);
     f1.wait();
     if constexpr (decltype(LD)::value) wait_loads<(NSTAGE - 2) * C::DMA>();
     __builtin_amdgcn_s_barrier();
@@ -413,22 +493,121 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   };
   auto loop = [&](auto LD) {
     const int common = nk / KG;
+    const int plain = LD && residual_dma ? max(common - NSTAGE, 0) : common;
     uint32_t st = 0;
-    for (int it = 0; it < common; ++it) st = body(LD, it, st);
+    int it = 0;
+    for (; it < plain; ++it) st = body(LD, it, st);
+    if constexpr (decltype(LD)::value && INPLACE)
+      for (; it < common; ++it) st = body(I2{}, it, st);
     if (KG > 1 && nk % KG) {
       if (count > common) body(LD, common, st);
       else __builtin_amdgcn_s_barrier();        // the other groups' last step
     }
   };
-  if (loader) loop(std::true_type{});
-  else loop(std::false_type{});
+  if (loader) loop(I1{});
+  else loop(I0{});
 
-  // Epilogue: slices of 32 tokens through LDS, so that a lane holds eight
-  // consecutive features of a token for the residual, the rounding and the
-  // store.  A lane's features are the same for every token.
   wait_loads<0>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+
+  if constexpr (INPLACE) {
+    // Epilogue in place: every value is finished in the accumulators' order,
+    // residual and rounding included, and goes into the wave's region as bf16;
+    // whole rows of the region then go out 16 B a lane.  The output streams past
+    // the L2, which it would only flush.
+    const float* sc = reinterpret_cast<const float*>(lds_all + NSTAGE * C::STAGE);
+    uint8_t* region = lds_all + (count + wave / C::RPS) % NSTAGE * C::STAGE + wave % C::RPS * C::REGION;
+    const int m_wave = m0 + wm * C::WTM, n_wave = n0 + wn * C::WTN;
+    const bool rows_full = m_wave + C::WTM <= args.M;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const float sx = sc[2 * BM + wn * C::WTN + 32 * j + nl];
+      const int n = n_wave + 32 * j + nl;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        float z[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int f = wm * C::WTM + 32 * i + 8 * q + 4 * h;
+          const f32x4 w = *reinterpret_cast<const f32x4*>(sc + f);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) z[4 * q + u] = acc[i][j][4 * q + u] * (sx * w[u]);
+        }
+        if (args.bias) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 b4 = *reinterpret_cast<const f32x4*>(sc + BM + wm * C::WTM + 32 * i + 8 * q + 4 * h);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) z[4 * q + u] += b4[u];
+          }
+        }
+        f8_act(z, args.act);
+        uint8_t* place[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          place[q] = region + (32 * j + nl) * (C::CH * 16) + (((4 * i + q) ^ (nl % C::CH)) * 16) + 8 * h;
+        if (residual_dma) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const u32x2 r = *reinterpret_cast<const u32x2*>(place[q]);
+            z[4 * q] += bf16_lo(r[0]);
+            z[4 * q + 1] += bf16_hi(r[0]);
+            z[4 * q + 2] += bf16_lo(r[1]);
+            z[4 * q + 3] += bf16_hi(r[1]);
+          }
+        } else if (args.residual && n < args.N) {
+          const uint16_t* r = (const uint16_t*)args.residual + (int64_t)n * args.ldr + m_wave + 32 * i + 4 * h;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (rows_full) {
+              const u32x2 v = *reinterpret_cast<const u32x2_a2*>(r + 8 * q);
+              z[4 * q] += bf16_lo(v[0]);
+              z[4 * q + 1] += bf16_hi(v[0]);
+              z[4 * q + 2] += bf16_lo(v[1]);
+              z[4 * q + 3] += bf16_hi(v[1]);
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (m_wave + 32 * i + 8 * q + 4 * h + u < args.M)
+                  z[4 * q + u] += __uint_as_float((uint32_t)r[8 * q + u] << 16);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<u32x2*>(place[q]) =
+              (u32x2){pack_bf16(z[4 * q], z[4 * q + 1]), pack_bf16(z[4 * q + 2], z[4 * q + 3])};
+      }
+      constexpr int PASSES = 32 * C::CH / 64;
+      const int m = m_wave + 8 * (lane % C::CH), left = args.M - m;
+      uint16_t* y = (uint16_t*)args.Y + (int64_t)(n_wave + 32 * j + r_t) * args.ldy + m;
+      u32x4 v[PASSES];
+#pragma unroll
+      for (int t = 0; t < PASSES; ++t) {
+        const int tn = t * (64 / C::CH) + r_t;
+        v[t] = *reinterpret_cast<const u32x4*>(region + (32 * j + tn) * (C::CH * 16) + ((lane % C::CH) ^ (tn % C::CH)) * 16);
+      }
+#pragma unroll
+      for (int t = 0; t < PASSES; ++t) {
+        if (n_wave + 32 * j + t * (64 / C::CH) + r_t >= args.N) continue;
+        uint16_t* p = y + (int64_t)t * (64 / C::CH) * args.ldy;
+        if (left >= 8) {
+          store_16b<true>(p, v[t]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (u < left) p[u] = (uint16_t)(v[t][u / 2] >> (16 * (u & 1)));
+        }
+      }
+    }
+    return;
+  }
+
+  // Epilogue by slices of 32 tokens through LDS as fp32, so that a lane holds
+  // eight consecutive features of a token for the residual, the rounding and the
+  // store; with split K the groups' parts meet here, summed in group order.  A
+  // lane's features are the same for every token.
   constexpr int LPT = C::WTM / 8, TPI = 64 / LPT;      // lanes per token, tokens per pass
   constexpr int U = KG > 1 ? 1 : 32 / TPI < 4 ? 32 / TPI : 4;        // tokens of a lane in flight at once
   constexpr int PARTS = C::GWAVES * 32 * C::PITCH;      // floats of one group's slices
@@ -445,8 +624,13 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) bs[i] = 0.0f;
-    load8(args.w_scale + m, left, ws);
-    if (args.bias) load8(args.bias + m, left, bs);
+    load_row<8>(args.w_scale + m, left, ws);
+    if (args.bias) load_row<8>(args.bias + m, left, bs);
+    // arrived here, so that no wait for them inside the loops below also waits for stores
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(ws[i]), "+v"(bs[i]));
+#pragma unroll
+    for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(sx[j]));
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       if (KG > 1 && j > 0) __syncthreads();
@@ -480,7 +664,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
           float r[U][8];
 #pragma unroll
           for (int t = 0; t < U; ++t)
-            load8((const OutT*)args.residual + (int64_t)(n + t * TPI) * args.ldr + m,
+            load_row<8>((const OutT*)args.residual + (int64_t)(n + t * TPI) * args.ldr + m,
                   full || n + t * TPI < args.N ? left : 0, r[t]);
 #pragma unroll
           for (int t = 0; t < U; ++t)
@@ -493,7 +677,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = z[8 * t + i];
-          store8<true>((OutT*)args.Y + (int64_t)(n + t * TPI) * args.ldy + m, left, v);
+          store_row<8, true>((OutT*)args.Y + (int64_t)(n + t * TPI) * args.ldy + m, left, v);
         }
       }
     }
@@ -533,9 +717,13 @@ static p24_status launch_tile(F8Args a, hipStream_t st) {
 // flight (64x64 in the last line 10.9 -> 9.2; 1000 x 4032 with 517 tokens, fp32,
 // 16.7 -> 12.2; 64x32 on 4096 x 4096 with 128 tokens 9.8 -> 7.7).  A group needs a
 // few steps of its own to be worth its part in the sum: K >= 1024.
-// At 128 tiles of 32 x 32 or fewer, no tile that shares operands in LDS fills the
-// chip, and the kernel without them is faster: 16 waves on each (4096 x 4096, one
-// token: 5.3, 64x32 6.5), 4 where K is under 1024.
+// A tile's steps wait for memory and for each other; the kernel without shared
+// operands does neither, but reads the tokens once per 32 rows.  It wins where
+// that is little: at most 128 tiles of 32 x 32 (4096 x 4096, one token 4.9, 64x32
+// 6.2; 1024 x 8192, one token 5.7, 8.5), at most 512 with a short K (4096 x 512, 128
+// tokens 3.8, 4.0; 1000 x 1024, 400 tokens 4.9, 5.2; but 8192 x 1024, 128 tokens 7.4,
+// 64x64 4.9), and with few tokens (16384 x 4096, one token 8.8, 64x64 9.6; but 24
+// tokens 11.4, 64x32 10.2).
 enum class F8Kernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x256 };
 
 static int64_t f8_blocks(const F8Args& a, int bm, int bn) {
@@ -553,13 +741,15 @@ static F8Kernel choose_f8(const F8Args& a, bool exact) {
     if (t == "256x128" || (t == "256x256" && exact)) return F8Kernel::T256x128;
     if (t == "256x256") return F8Kernel::T256x256;
   }
+  const int64_t tiles = f8_blocks(a, 32, 32);
+  if (tiles <= 128 || a.N <= 8 || (tiles <= 512 && a.K <= 1024)) return F8Kernel::TOKENS;
   // the widened operands of an fp32 output do not fit the registers of 256 x 256
   if (!exact && f8_blocks(a, 256, 256) >= 144) return F8Kernel::T256x256;
   if (f8_blocks(a, 256, 128) >= 160) return F8Kernel::T256x128;
   if (f8_blocks(a, 128, 128) >= 160) return F8Kernel::T128x128;
   if (f8_blocks(a, 128, 64) >= 160) return F8Kernel::T128x64;
   if (f8_blocks(a, 64, 64) >= 144) return F8Kernel::T64x64;
-  return f8_blocks(a, 32, 32) > 128 ? F8Kernel::T64x32 : F8Kernel::TOKENS;
+  return F8Kernel::T64x32;
 }
 
 template <typename OutT>
@@ -582,7 +772,10 @@ static p24_status launch_f8(const F8Args& a, hipStream_t st) {
       return launch_tile<64, 32, 2, 1, 2, 1, OutT>(a, st);
     case F8Kernel::TOKENS: break;
   }
-  if (long_k) return launch_tokens<16, OutT>(a, st);
+  // waves that split K: 4.9, 5.1 and 6.2 us with 16, 8 and 4 (4096 x 4096, one token);
+  // 10.5, 8.8 and 9.4 (16384 x 4096); 4.8, 3.5 and 3.4 (500 x 256, 700 tokens)
+  if (a.K >= 2048 && f8_blocks(a, 32, 32) <= 256) return launch_tokens<16, OutT>(a, st);
+  if (a.K >= 1024) return launch_tokens<8, OutT>(a, st);
   return launch_tokens<4, OutT>(a, st);
 }
 
@@ -631,6 +824,7 @@ extern "C" P24_API p24_status spmm24_f8(const void* data, const float* w_scale, 
   a.N = (int)N;
   a.K = (int)K;
   a.act = act;
+  a.res_dma = residual && aligned(residual, 16) && ldr % 8 == 0 && M % 8 == 0 && (uint64_t)ldr * 1024 < (1ull << 32);
   if (y_dtype == P24_F32) return launch_f8<float>(a, (hipStream_t)stream);
   return launch_f8<uint16_t>(a, (hipStream_t)stream);
 }

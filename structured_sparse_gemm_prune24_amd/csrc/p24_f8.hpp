@@ -23,6 +23,7 @@ typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
 
 // Row storage types: fp32, bf16 bits, e4m3 bits.
 struct f8_t {
@@ -93,28 +94,39 @@ __device__ __forceinline__ void f8_act(float (&z)[N], int act) {
   }
 }
 
-// Eight consecutive values from p, `left` of them inside the row.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
-  if (left >= 8) {
+// V consecutive values from p, `left` of them inside the row (the others read as
+// zero).  Any element alignment.
+template <int V, typename T>
+__device__ __forceinline__ void load_row(const T* p, int left, float (&v)[V]) {
+  static_assert(V % 4 == 0 && (sizeof(T) == 4 || V == 8 || V == 4), "whole vectors");
+  if (left >= V) {
     if constexpr (sizeof(T) == 2) {
-      const u32x4 w = *reinterpret_cast<const u32x4_a2*>(p);
+      uint32_t w[V / 2];
+      if constexpr (V == 8) {
+        const u32x4 x = *reinterpret_cast<const u32x4_a2*>(p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) w[i] = x[i];
+      } else {
+        const u32x2 x = *reinterpret_cast<const u32x2_a2*>(p);
+        w[0] = x[0];
+        w[1] = x[1];
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
         v[2 * i] = bf16_lo(w[i]);
         v[2 * i + 1] = bf16_hi(w[i]);
       }
     } else {
-      const u32x4 lo = *reinterpret_cast<const u32x4_a4*>(p), hi = *reinterpret_cast<const u32x4_a4*>(p + 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(lo[i]);
-        v[4 + i] = __uint_as_float(hi[i]);
+      for (int q = 0; q < V / 4; ++q) {
+        const u32x4 x = *reinterpret_cast<const u32x4_a4*>(p + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * q + i] = __uint_as_float(x[i]);
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < V; ++i) {
       v[i] = 0.0f;
       if (i < left) {
         if constexpr (sizeof(T) == 2) v[i] = __uint_as_float((uint32_t)p[i] << 16);
@@ -130,42 +142,44 @@ __device__ __forceinline__ void store_16b(void* p, u32x4 v) {
   if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
   else *reinterpret_cast<u32x4_a2*>(p) = v;
 }
-template <bool NT = false, typename T>
-__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
-  if constexpr (sizeof(T) == 1) {
-    const uint32_t lo = pack_f8(v[0], v[1], v[2], v[3]), hi = pack_f8(v[4], v[5], v[6], v[7]);
-    if (left >= 8) {
-      *reinterpret_cast<u32x2_a1*>(p) = (u32x2){lo, hi};
+
+// V consecutive values to p, rounded to nearest even, `left` of them inside the row.
+template <int V, bool NT = false, typename T>
+__device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V]) {
+  if constexpr (sizeof(T) == 4) {
+    if (left >= V) {
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[4 * q + i]);
+        store_16b<NT>(p + 4 * q, w);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i].v = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
-    }
-  } else if constexpr (sizeof(T) == 2) {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    if (left >= 8) {
-      store_16b<NT>(p, w);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+      for (int i = 0; i < V; ++i)
+        if (i < left) p[i] = v[i];
     }
   } else {
-    if (left >= 8) {
-      u32x4 lo, hi;
+    constexpr int PER = 4 / sizeof(T), W = V / PER;    // values per word, words
+    uint32_t w[W];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = __float_as_uint(v[i]);
-        hi[i] = __float_as_uint(v[4 + i]);
-      }
-      store_16b<NT>(p, lo);
-      store_16b<NT>(p + 4, hi);
+    for (int i = 0; i < W; ++i) {
+      if constexpr (sizeof(T) == 1) w[i] = pack_f8(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      else w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+    if (left >= V) {
+      if constexpr (W == 4) store_16b<NT>(p, (u32x4){w[0], w[1], w[2], w[3]});
+      else if constexpr (W == 2) *reinterpret_cast<u32x2_a1*>(p) = (u32x2){w[0], w[1]};
+      else *reinterpret_cast<u32_a1*>(p) = w[0];
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = v[i];
+      for (int i = 0; i < V; ++i)
+        if (i < left) {
+          const uint32_t x = w[i / PER] >> (8 * sizeof(T) * (i % PER));
+          if constexpr (sizeof(T) == 1) p[i].v = (uint8_t)x;
+          else p[i] = (uint16_t)x;
+        }
     }
   }
 }

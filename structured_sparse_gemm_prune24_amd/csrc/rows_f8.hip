@@ -1,7 +1,7 @@
 // Row operators around the 8-bit products: RMS norm with the residual's
 // addition, and the gated activation, each with an 8-bit, bf16 or fp32 output.
 //
-// One row (token) belongs to G threads, E chunks of 8 consecutive values each,
+// One row (token) belongs to G threads, E chunks of 16 input bytes each,
 // held in registers from the one read to the one write: the row's statistics
 // (sum of squares, largest magnitude) need the whole row before the first
 // output, and a second read would cost what the first did.  Bound by HBM: the
@@ -59,10 +59,11 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
 }
 
 // G threads a row; a block of 256 threads holds four rows where G is a wave.
-template <int G> constexpr int ROW_BLOCK = G < 256 ? 256 : G;
+template <int G> constexpr int ROW_BLOCK = G == 64 ? 256 : G;
 
 template <typename T, typename OutT, int G, int E, bool NORM>
 __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
+  constexpr int V = 16 / sizeof(T);   // values of a chunk: 16 bytes of input
   const int t = threadIdx.x % G;
   const int64_t row = (int64_t)blockIdx.x * (ROW_BLOCK<G> / G) + threadIdx.x / G;
   if (row >= args.rows) return;   // whole waves, and whole blocks where G spans waves
@@ -70,50 +71,49 @@ __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
   const T* a = (const T*)args.a + row * args.lda;
   const T* b = args.b ? (const T*)args.b + row * args.ldb : nullptr;
 
-  float v[E][8];
-  float sum = 0.0f;
-  uint32_t top = 0;
+  float v[E][V], u[E][V], w[NORM ? E : 1][V];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int c = (t + e * G) * 8;
-    load8(a + c, width - c, v[e]);
+    const int c = (t + e * G) * V;
+    load_row<V>(a + c, width - c, v[e]);
+    if (b) load_row<V>(b + c, width - c, u[e]);
+  }
+  // the weights are asked for ahead of the sum's store, which the compiler must keep in its place
+  if constexpr (NORM) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = (t + e * G) * V;
+      load_row<V>(args.weight + c, width - c, w[e]);
+    }
+  }
+  if constexpr (!NORM) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f8_act(v[e], args.act);
   }
   if (b) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int c = (t + e * G) * 8;
-      float u[8];
-      load8(b + c, width - c, u);
-      if constexpr (NORM) {
+      const int c = (t + e * G) * V;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[e][i] += u[i];
-        store8((T*)args.h + row * args.ldh + c, width - c, v[e]);
-      } else {
-        f8_act(v[e], args.act);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[e][i] *= u[i];
-      }
+      for (int i = 0; i < V; ++i) v[e][i] = NORM ? v[e][i] + u[e][i] : v[e][i] * u[e][i];
+      if constexpr (NORM) store_row<V>((T*)args.h + row * args.ldh + c, width - c, v[e]);
     }
-  } else if constexpr (!NORM) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) f8_act(v[e], args.act);
   }
   // values past the row are zero: act(0) = 0 for every activation
+  float sum = 0.0f;
+  uint32_t top = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int c = (t + e * G) * 8;
     if constexpr (NORM) {
-      float w[8];
-      load8(args.weight + c, width - c, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < V; ++i) {
         sum = fmaf(v[e][i], v[e][i], sum);
-        v[e][i] *= w[i];
+        v[e][i] *= w[e][i];
       }
     }
     if constexpr (sizeof(OutT) == 1) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, mag(v[e][i]));
+      for (int i = 0; i < V; ++i) top = max(top, mag(v[e][i]));
     }
   }
   // two factors, not their product: with a tiny scale the product overflows
@@ -130,13 +130,13 @@ __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
   OutT* y = (OutT*)args.y + row * args.ldy;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int c = (t + e * G) * 8;
+    const int c = (t + e * G) * V;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < V; ++i) {
       if constexpr (NORM) v[e][i] *= k;
       if constexpr (sizeof(OutT) == 1) v[e][i] *= inv;
     }
-    store8(y + c, width - c, v[e]);
+    store_row<V>(y + c, width - c, v[e]);
   }
 }
 
@@ -147,16 +147,34 @@ static p24_status launch_rows(const RowArgs& a, hipStream_t st) {
   return launch_status();
 }
 
+// Threads and chunks of a row, by its count of 16-byte chunks: as few chunks a
+// thread as a block of 512 or 1024 allows, because a row's time is its trips to
+// memory and the reduction.  Measured, us (bf16 unless said):
+//   norm 8192 x 8192   512 x 2 89.4 (5.3 TB/s), 256 x 4 100.7, 1024 x 1 89.2
+//   gate 4096 x 8192   512 x 2 31.6 (5.3 TB/s), 256 x 4 35.8, 1024 x 1 34.5
+//   norm 4096 x 4096 fp32   1024 x 1 39.8, 512 x 2 41.9;  gate 777 x 2051 fp32  6.0, 6.5
+//   gate 2000 x 4096   512 x 1 9.6, 256 x 2 10.2;  norm 1 x 4096  3.3, 3.5
+//   norm 8192 x 1024   64 x 2 12.4, 128 x 1 13.8, 256 x 1 15.7;  norm 2 x 700  128 x 1 3.8, 64 x 2 4.3
 template <typename T, typename OutT, bool NORM>
 static p24_status rows_by_width(const RowArgs& a, hipStream_t st) {
-  const int w = a.width;
-  if (w <= 512) return launch_rows<T, OutT, 64, 1, NORM>(a, st);
-  if (w <= 2048) return launch_rows<T, OutT, 256, 1, NORM>(a, st);
-  if (w <= 4096) return launch_rows<T, OutT, 256, 2, NORM>(a, st);
-  if (w <= 8192) return launch_rows<T, OutT, 256, 4, NORM>(a, st);
-  if (w <= 16384) return launch_rows<T, OutT, 1024, 2, NORM>(a, st);
-  if (w <= 32768) return launch_rows<T, OutT, 1024, 4, NORM>(a, st);
-  return launch_rows<T, OutT, 1024, 8, NORM>(a, st);
+  constexpr int V = 16 / sizeof(T);
+  const int chunks = (a.width + V - 1) / V;
+  if (chunks <= 64) return launch_rows<T, OutT, 64, 1, NORM>(a, st);
+  if (chunks <= 128) {
+    if (a.rows >= 1024) return launch_rows<T, OutT, 64, 2, NORM>(a, st);   // four rows a block, no barrier
+    return launch_rows<T, OutT, 128, 1, NORM>(a, st);
+  }
+  if (chunks <= 256) return launch_rows<T, OutT, 256, 1, NORM>(a, st);
+  if (chunks <= 512) return launch_rows<T, OutT, 512, 1, NORM>(a, st);
+  if (chunks <= 1024) {
+    if constexpr (sizeof(T) == 4) return launch_rows<T, OutT, 1024, 1, NORM>(a, st);
+    else return launch_rows<T, OutT, 512, 2, NORM>(a, st);
+  }
+  if (chunks <= 2048) return launch_rows<T, OutT, 1024, 2, NORM>(a, st);
+  if (chunks <= 4096) return launch_rows<T, OutT, 1024, 4, NORM>(a, st);
+  if (chunks <= 8192) return launch_rows<T, OutT, 1024, 8, NORM>(a, st);
+  if constexpr (sizeof(T) == 4) return launch_rows<T, OutT, 1024, 16, NORM>(a, st);
+  else return P24_ERR_SHAPE;
 }
 
 template <bool NORM>

@@ -221,7 +221,8 @@ TILES = ["tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x256"]
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("N,M,K", [(1, 1, 64), (33, 65, 128), (70, 300, 192), (129, 257, 448), (257, 260, 1024),
-                                   (100, 129, 1088), (300, 513, 1472), (64, 128, 4160)])
+                                   (100, 129, 1088), (300, 513, 1472), (64, 128, 4160), (300, 520, 64),
+                                   (260, 264, 256), (90, 272, 384), (513, 512, 512)])
 @pytest.mark.parametrize("tile", TILES)
 def test_product_of_every_kernel(monkeypatch, tile, N, M, K, out):
     """Each kernel at tokens, rows and K off its tile, K's parts within a block even and uneven; rows that the
@@ -239,6 +240,17 @@ def test_product_of_every_kernel(monkeypatch, tile, N, M, K, out):
     bias = _rows(6, 1, M, 0, torch.float32)[0].contiguous()
     for name in ("gelu", "silu"):
         _check_product(c, x, bias=bias, name=name, r=r, out=out)
+    # a residual of whole 16-byte chunks, in place, next to the same one at odd rows
+    if M % 8 == 0:
+        r8 = _rows(5, N, M, 8, out)
+        assert torch.equal(p24.spmm24_f8(c, x, residual=r8, out=r8.clone()), p24.spmm24_f8(c, x, residual=r8, out_dtype=out))
+        odd = _rows(5, N, M, 9, out)
+        odd.copy_(r8)
+        assert torch.equal(p24.spmm24_f8(c, x, residual=odd, bias=bias, out_dtype=out),
+                           p24.spmm24_f8(c, x, residual=r8, bias=bias, out_dtype=out))
+        place = r8.clone()
+        assert torch.equal(p24.spmm24_f8(c, x, residual=place, bias=bias, act="gelu", out=place),
+                           p24.spmm24_f8(c, x, residual=r8, bias=bias, act="gelu", out_dtype=out))
 
 
 @pytest.mark.parametrize("N,M,K", [(1, 64, 128), (5, 130, 4160), (40, 200, 192), (300, 300, 832), (600, 1500, 640)])
