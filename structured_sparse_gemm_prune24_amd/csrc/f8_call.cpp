@@ -62,6 +62,24 @@ at::Tensor make(std::initializer_list<int64_t> shape, at::ScalarType type, const
   return at::detail::empty_cuda(at::IntArrayRef(shape.begin(), shape.size()), type, dev, std::nullopt);
 }
 
+// A new tokens x width output; in 8 bits its scales lie behind the values in the
+// same allocation (the two are used and freed together, and one allocation is
+// half a microsecond less).
+at::Tensor make_rows(int64_t tokens, int64_t width, int code, const at::Device& dev, at::Tensor& scale) {
+  if (code != P24_F8) return make({tokens, width}, type_of(code), dev);
+  const int64_t at = (tokens * width + 15) / 16 * 16;
+  const at::Tensor buf = make({at + 4 * tokens}, at::kByte, dev);
+  auto part = [&](at::ScalarType type, std::initializer_list<int64_t> shape, int64_t first) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(c10::IntArrayRef(shape.begin(), shape.size()));
+    t.unsafeGetTensorImpl()->set_storage_offset(first);
+    return t;
+  };
+  scale = part(at::kFloat, {tokens}, at / 4);
+  return part(F8, {tokens, width}, 0);
+}
+
 void* stream_of(const at::Device& dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
 PyObject* none() { Py_RETURN_NONE; }
@@ -108,8 +126,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!w || !PyFloat_CheckExact(a[3])) return none();
     if (!is_none(a[2]) && (!rows(a[2], r, ldr) || !same_rows(*r, *x))) return none();
     const long code = PyLong_AsLong(a[4]);
-    at::Tensor y = make({tokens, width}, type_of((int)code), dev), s, h;
-    if (code == P24_F8) s = make({tokens}, at::kFloat, dev);
+    at::Tensor s, h, y = make_rows(tokens, width, (int)code, dev, s);
     if (r) h = make({tokens, width}, x->scalar_type(), dev);
     const p24_status st =
         p_norm(x->data_ptr(), xc, ldx, r ? r->data_ptr() : nullptr, ldr, w, (float)PyFloat_AS_DOUBLE(a[3]), tokens,
@@ -132,8 +149,7 @@ PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t tokens = g->size(0), width = g->size(1);
     const at::Device dev = g->device();
     const long act = PyLong_AsLong(a[2]), code = PyLong_AsLong(a[3]);
-    at::Tensor y = make({tokens, width}, type_of((int)code), dev), s;
-    if (code == P24_F8) s = make({tokens}, at::kFloat, dev);
+    at::Tensor s, y = make_rows(tokens, width, (int)code, dev, s);
     const p24_status st = p_gate(g->data_ptr(), xc, ldg, u ? u->data_ptr() : nullptr, ldu, (int)act, tokens, width,
                                  y.data_ptr(), (int)code, width, s.defined() ? (float*)s.data_ptr() : nullptr,
                                  stream_of(dev));

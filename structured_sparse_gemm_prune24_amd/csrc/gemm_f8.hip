@@ -705,9 +705,11 @@ static p24_status launch_tile(F8Args a, hipStream_t st) {
 // Which kernel.  A block tile's loads per multiply shrink with its size, but a
 // launch needs enough blocks for 256 CUs: the largest tile that still gives about
 // five eighths of them wins (144 blocks for 256 x 256, whose loads are the
-// fewest).  Measured, us, M x K with N tokens:
+// fewest; 256 x 192 where it fills one round better).  Measured, us, M x K with N tokens:
 //   8192 x 8192, 8192   256x256 264, 256x128 358, 128x128 421
-//   2304 x 768, 4096    256x256 12.6 (144 blocks), 128x128 14.0
+//   2304 x 768, 4096    256x192 11.8 (198 blocks), 256x256 13.2 (144), 128x128 14.3
+//   4096 x 2048, 2048   256x192 17.0 (176 blocks), 256x128 17.4 (256), 256x256 18.6 (128)
+//   2048 x 1024, 6144   256x256 15.4 (192 blocks), 256x192 23.6 (256)
 //   8192 x 4096, 1024   256x128 24.1 (256 blocks), 128x128 28.5, 256x256 28.2
 //   768 x 768, 4096     128x128 6.3 (192 blocks), 256x128 7.7, 64x64 7.3
 //   4096 x 4096, 512    128x64 12.4 (256 blocks), 128x128 14.2, 64x64 13.6
@@ -724,7 +726,7 @@ static p24_status launch_tile(F8Args a, hipStream_t st) {
 // tokens 3.8, 4.0; 1000 x 1024, 400 tokens 4.9, 5.2; but 8192 x 1024, 128 tokens 7.4,
 // 64x64 4.9), and with few tokens (16384 x 4096, one token 8.8, 64x64 9.6; but 24
 // tokens 11.4, 64x32 10.2).
-enum class F8Kernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x256 };
+enum class F8Kernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x192, T256x256 };
 
 static int64_t f8_blocks(const F8Args& a, int bm, int bn) {
   return ((a.M + (int64_t)bm - 1) / bm) * ((a.N + (int64_t)bn - 1) / bn);
@@ -738,13 +740,18 @@ static F8Kernel choose_f8(const F8Args& a, bool exact) {
     if (t == "64x64") return F8Kernel::T64x64;
     if (t == "128x64") return F8Kernel::T128x64;
     if (t == "128x128") return F8Kernel::T128x128;
-    if (t == "256x128" || (t == "256x256" && exact)) return F8Kernel::T256x128;
+    if (t == "256x128" || (exact && (t == "256x192" || t == "256x256"))) return F8Kernel::T256x128;
+    if (t == "256x192") return F8Kernel::T256x192;
     if (t == "256x256") return F8Kernel::T256x256;
   }
   const int64_t tiles = f8_blocks(a, 32, 32);
   if (tiles <= 128 || a.N <= 8 || (tiles <= 512 && a.K <= 1024)) return F8Kernel::TOKENS;
-  // the widened operands of an fp32 output do not fit the registers of 256 x 256
-  if (!exact && f8_blocks(a, 256, 256) >= 144) return F8Kernel::T256x256;
+  // the widened operands of an fp32 output do not fit the registers of the two widest
+  if (!exact) {
+    const int64_t n256 = f8_blocks(a, 256, 256), n192 = f8_blocks(a, 256, 192);
+    if (n256 < 160 && n192 >= 160 && n192 <= 224) return F8Kernel::T256x192;
+    if (n256 >= 144) return F8Kernel::T256x256;
+  }
   if (f8_blocks(a, 256, 128) >= 160) return F8Kernel::T256x128;
   if (f8_blocks(a, 128, 128) >= 160) return F8Kernel::T128x128;
   if (f8_blocks(a, 128, 64) >= 160) return F8Kernel::T128x64;
@@ -759,6 +766,8 @@ static p24_status launch_f8(const F8Args& a, hipStream_t st) {
   switch (choose_f8(a, EXACT)) {
     case F8Kernel::T256x256:
       if constexpr (!EXACT) return launch_tile<256, 256, 2, 4, 4, 1, OutT>(a, st);
+    case F8Kernel::T256x192:
+      if constexpr (!EXACT) return launch_tile<256, 192, 4, 2, 4, 1, OutT>(a, st);
     case F8Kernel::T256x128: return launch_tile<256, 128, 4, 2, 4, 1, OutT>(a, st);
     case F8Kernel::T128x128: return launch_tile<128, 128, 2, 4, 4, 1, OutT>(a, st);
     case F8Kernel::T128x64:

@@ -216,7 +216,7 @@ def test_product(N, M, K, out):
     _check_product(c, x, r=r, out=out)
 
 
-TILES = ["tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x256"]
+TILES = ["tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x192", "256x256"]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
