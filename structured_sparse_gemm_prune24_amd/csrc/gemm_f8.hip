@@ -170,20 +170,26 @@ struct F8Tile {
   static constexpr int WTM = BM / WGM, WTN = BN / WGN;     // wave tile
   static constexpr int TM = WTM / 32, TN = WTN / 32;       // its 32 x 32 tiles
   static constexpr int LW = LW_;                           // waves of a group that load
-  // stage: [X: BN rows of 128 B | per row group: two 64-k blocks of (row blocks' values, 1 KiB of positions)]
+  // stage: [X: BN rows of 128 B | per row group: two 64-k blocks of (row blocks' values, 1 KiB of positions)],
+  // with half a row group [.. | two row blocks' values of either 64-k block | 512 B of positions of each]
   static constexpr int GROUPS = BM >= 128 ? BM / 128 : 1;
   static constexpr int RBG = BM >= 128 ? 4 : BM / 32;      // row blocks used of a group
-  static constexpr int BLOCK = (RBG + 1) * 1024;           // one 64-k block of a group in LDS
-  static constexpr int X_BYTES = BN * 128, A_BYTES = GROUPS * 2 * BLOCK;
+  static constexpr int UNITS = RBG == 4 ? 10 : 2 * RBG + 1;   // 1 KiB loads of a group's step
+  static constexpr int BLOCK = RBG == 4 ? 5120 : RBG * 1024;  // from one 64-k block's values to the next's
+  static constexpr int P_FIRST = RBG == 4 ? 4096 : 2 * BLOCK, P_NEXT = RBG == 4 ? BLOCK : 512;   // the same of positions
+  static constexpr int X_BYTES = BN * 128, A_BYTES = GROUPS * UNITS * 1024;
   static constexpr int STAGE = X_BYTES + A_BYTES;
   static constexpr int NSTAGE = 3 * KG * STAGE <= 160 * 1024 ? 3 : 2;
   static constexpr int X_DMA = BN / 8 / LW;                // 1 KiB loads per loading wave and step
   static constexpr int A_LOADS = A_BYTES / 1024;
-  static constexpr int A_DMA = (A_LOADS + LW - 1) / LW;    // the last ones may repeat a load
+  // A remainder of one load is left to one wave; of two, the other two waves repeat
+  // a load, which is cheaper than uneven counts (4096 x 2304 x 768 in 128 x 128: 13.9 us, 14.9).
+  static constexpr int A_DMA = (A_LOADS + LW - 1) / LW;
+  static constexpr int A_LAST = A_LOADS % LW == 1 ? 1 : 0;   // waves that issue the last one (0: all)
   static constexpr int DMA = X_DMA + A_DMA;
   static_assert(BM % (32 * WGM) == 0 && BN % (32 * WGN) == 0, "whole 32 x 32 tiles per wave");
   static_assert((BN / 8) % LW == 0 && LW % 2 == 0 && LW <= GWAVES, "even X loads");
-  static_assert(BM % 128 == 0 || BM == 64 || BM == 32, "whole row groups, or an aligned part of one");
+  static_assert(BM % 128 == 0 || BM == 64, "whole row groups, or half of one");
   static_assert(NSTAGE * KG * STAGE <= 160 * 1024, "LDS");
   static_assert(NSTAGE * DMA < 64, "vmcnt range");
   // epilogue by slices (fp32 outputs, split K): each wave turns one 32-token slice at a time through LDS
@@ -314,22 +320,26 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   const uint32_t x_voff = (uint32_t)(x_row * ldx + 16 * x_chunk);
   const uint32_t x_tail = x_voff - ((args.K & 64) && x_chunk >= 4 ? 64 : 0);
   const uint32_t x_jump = (uint32_t)(8 * C::LW * ldx);
-  // weights: load q is block q % (RBG + 1) of 64-k block (q / (RBG + 1)) % 2 of row group q / (2 (RBG + 1))
+  // weights: load q is unit q % UNITS of row group q / UNITS: the pieces of its two
+  // 64-k blocks in order, or of half a group two row blocks' values of each, then
+  // the positions, 512 B of either
   const int g0 = m0 / 128;
   const int g_count = min((int)f8_groups(args.M) - g0, C::GROUPS);
   const __amdgpu_buffer_rsrc_t a_rsrc =
       f8_rsrc(args.W + (int64_t)g0 * steps * F8_PIECE, (uint32_t)g_count * steps * F8_PIECE);
   const uint32_t a_voff = (uint32_t)lane * 16;
+  const uint32_t p_voff = (uint32_t)(lane / 32) * F8_PIECE + (uint32_t)(lane % 32) * 16;
+  const uint32_t first_rb = (uint32_t)(m0 / 32) % 4;        // half a group: its first row block
   uint32_t a_soff[C::A_DMA], a_dst[C::A_DMA];
 #pragma unroll
   for (int j = 0; j < C::A_DMA; ++j) {
-    const int q = min(j * C::LW + wave, C::A_LOADS - 1);
-    const int grp = q / (2 * (C::RBG + 1)), u = q % (2 * (C::RBG + 1));
-    const int s = u / (C::RBG + 1), v = u % (C::RBG + 1);
-    const int part = v == C::RBG ? 4 : (m0 / 32) % 4 + v;     // positions after the values
-    a_soff[j] = ((uint32_t)grp * steps + s) * F8_PIECE + part * 1024;
+    const int q = min(j * LW + wave, C::A_LOADS - 1), u = q % C::UNITS;
     a_dst[j] = C::X_BYTES + q * 1024;
+    const uint32_t grp = (uint32_t)(q / C::UNITS) * steps * F8_PIECE;
+    if constexpr (C::RBG == 4) a_soff[j] = grp + u * 1024;
+    else a_soff[j] = u == 2 * C::RBG ? 4096 + first_rb * 256 : (u / C::RBG) * F8_PIECE + (first_rb + u % C::RBG) * 1024;
   }
+  const bool last_load = C::A_LAST == 0 || wave < C::A_LAST;
   const bool loader = wave < C::LW;
 
   // load Q of a loading wave for the group's step `it` (its last one past the end) into the stage at byte st
@@ -342,7 +352,9 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
       load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, voff, (uint32_t)g * 128 + q * x_jump);
     } else {
       constexpr int j = q - C::X_DMA;
-      load_to_lds(a_rsrc, stage + a_dst[j], a_voff, (uint32_t)g * (2 * F8_PIECE) + a_soff[j]);
+      if (C::A_LAST != 0 && j == C::A_DMA - 1 && !last_load) return;
+      const uint32_t voff = C::RBG < 4 && (j * LW + wave) % C::UNITS == 2 * C::RBG ? p_voff : a_voff;
+      load_to_lds(a_rsrc, stage + a_dst[j], voff, (uint32_t)g * (2 * F8_PIECE) + a_soff[j]);
     }
   };
 
@@ -382,9 +394,9 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
       b_addr[ss][q] = lds_base + b_row + (uint32_t)((c ^ (nl & 7)) * 16) + (EXACT ? 8 * h : 0);
     }
   // row blocks wm * TM .. of the tile: group wm * TM / RBG (a wave's rows lie in one group, or are whole groups)
-  const uint32_t a_group = lds_base + C::X_BYTES + (uint32_t)(wm * TM / C::RBG) * (2 * C::BLOCK);
+  const uint32_t a_group = lds_base + C::X_BYTES + (uint32_t)(wm * TM / C::RBG) * (C::UNITS * 1024);
   const uint32_t a_addr = a_group + (uint32_t)(wm * TM % C::RBG) * 1024 + lane * 16;
-  const uint32_t p_addr = a_group + C::RBG * 1024 + (uint32_t)((m0 / 32 + wm * TM) % 4) * 256 + lane * 4;
+  const uint32_t p_addr = a_group + C::P_FIRST + (uint32_t)(wm * TM % C::RBG) * 256 + lane * 4;
   static_assert(TM <= C::RBG ? C::RBG % TM == 0 : TM % C::RBG == 0, "a wave's row blocks and row groups nest");
 
   // read r of the TM + TM + TN * PIECES of 64-k block SS of the stage at byte `st`
@@ -392,11 +404,11 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   auto read_one = [&](auto SS, auto R, uint32_t st, Frags& f) {
     constexpr int ss = decltype(SS)::value, r = decltype(R)::value;
     if constexpr (r < TM) {
-      constexpr int off = (r / C::RBG) * 2 * C::BLOCK + ss * C::BLOCK + (r % C::RBG) * 256;
+      constexpr int off = (r / C::RBG) * C::UNITS * 1024 + ss * C::P_NEXT + (r % C::RBG) * 256;
       f.pos[r] = lds_b32<off>(p_addr + st);
     } else if constexpr (r < 2 * TM) {
       constexpr int i = r - TM;
-      constexpr int off = (i / C::RBG) * 2 * C::BLOCK + ss * C::BLOCK + (i % C::RBG) * 1024;
+      constexpr int off = (i / C::RBG) * C::UNITS * 1024 + ss * C::BLOCK + (i % C::RBG) * 1024;
       f.a[i] = lds_b128<off>(a_addr + st);
     } else {
       constexpr int j = (r - 2 * TM) / Frags::PIECES, q = (r - 2 * TM) % Frags::PIECES;
@@ -448,6 +460,12 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
+  // until at most n steps' loads of this wave are in flight
+  auto wait_steps = [&](auto N) {
+    constexpr int n = decltype(N)::value;
+    if (last_load) wait_loads<n * C::DMA>();
+    else wait_loads<n * (C::DMA - 1)>();
+  };
   const bool residual_dma = INPLACE && args.res_dma;
   if constexpr (INPLACE) {
     // scales and bias, 64 at a time, ahead of everything else
@@ -467,7 +485,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
       if (residual_dma && g >= count) static_for<0, C::DMA>([&](auto Q) { issue_residual(Q, g, g * C::STAGE); });
       else static_for<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE); });
     }
-  wait_loads<(NSTAGE - 1) * C::DMA>();
+  wait_steps(std::integral_constant<int, NSTAGE - 1>{});
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   Frags f0, f1;
@@ -483,7 +501,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     const uint32_t nx = st == (NSTAGE - 1) * C::STAGE ? 0 : st + C::STAGE;
     block(I0{}, f0, f1, I1{}, st, 0, 0);
     f1.wait();
-    if constexpr (decltype(LD)::value) wait_loads<(NSTAGE - 2) * C::DMA>();
+    if constexpr (decltype(LD)::value) wait_steps(std::integral_constant<int, NSTAGE - 2>{});
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
