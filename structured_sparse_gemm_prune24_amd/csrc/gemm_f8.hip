@@ -121,21 +121,16 @@ __global__ __launch_bounds__(W * 64) void k_f8_tokens(const F8Args args) {
 
   constexpr int U = 4;
   f32x16 acc = {};
-  int s = wave;
-  for (; s + (U - 1) * W < blocks; s += U * W) {
+  for (int s = wave; s < blocks; s += U * W) {
     F8Block<EXACT> b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t at = s + u * W;
-      b[u].load(w + at * F8_PIECE, p + at * F8_PIECE, x + at * 64, half);
+      if (u == 0 || at < blocks) b[u].load(w + at * F8_PIECE, p + at * F8_PIECE, x + at * 64, half);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = b[u].product(acc);
-  }
-  for (; s < blocks; s += W) {
-    F8Block<EXACT> b;
-    b.load(w + (int64_t)s * F8_PIECE, p + (int64_t)s * F8_PIECE, x + (int64_t)s * 64, half);
-    acc = b.product(acc);
+    for (int u = 0; u < U; ++u)
+      if (u == 0 || s + u * W < blocks) acc = b[u].product(acc);
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -532,16 +527,40 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   if constexpr (INPLACE) {
     // Epilogue in place: every value is finished in the accumulators' order,
     // residual and rounding included, and goes into the wave's region as bf16;
-    // whole rows of the region then go out 16 B a lane.  The output streams past
-    // the L2, which it would only flush.
+    // whole rows of the region then go out 16 B a lane.
     const float* sc = reinterpret_cast<const float*>(lds_all + NSTAGE * C::STAGE);
     uint8_t* region = lds_all + (count + wave / C::RPS) % NSTAGE * C::STAGE + wave % C::RPS * C::REGION;
     const int m_wave = m0 + wm * C::WTM, n_wave = n0 + wn * C::WTN;
-    const bool rows_full = m_wave + C::WTM <= args.M;
+    const int m = m_wave + 8 * (lane % C::CH), left = args.M - m;     // a lane's features of a whole row
+    constexpr int PASSES = 32 * C::CH / 64;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const float sx = sc[2 * BM + wn * C::WTN + 32 * j + nl];
-      const int n = n_wave + 32 * j + nl;
+      uint8_t* slice = region + 32 * j * (C::CH * 16);
+      const int n = n_wave + 32 * j + r_t;                              // a lane's first token of the slice
+      auto chunk = [&](int t) { return slice + t * (C::CH * 16) + ((lane % C::CH) ^ (t % C::CH)) * 16; };
+      if (args.residual && !residual_dma) {     // rows at any alignment come through registers
+        constexpr int B = PASSES < 4 ? PASSES : 4;
+#pragma unroll 1
+        for (int t0 = 0; t0 < PASSES; t0 += B) {
+          u32x4 r[B];
+#pragma unroll
+          for (int t = 0; t < B; ++t) {
+            const int step = (t0 + t) * (64 / C::CH);
+            const uint16_t* p = (const uint16_t*)args.residual + (int64_t)(n + step) * args.ldr + m;
+            r[t] = (u32x4){0, 0, 0, 0};
+            if (n + step < args.N && left >= 8) {
+              r[t] = *reinterpret_cast<const u32x4_a2*>(p);
+            } else if (n + step < args.N) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                if (u < left) r[t][u / 2] |= (uint32_t)p[u] << (16 * (u & 1));
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < B; ++t) *reinterpret_cast<u32x4*>(chunk((t0 + t) * (64 / C::CH) + r_t)) = r[t];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         float z[16];
@@ -564,8 +583,8 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
         uint8_t* place[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          place[q] = region + (32 * j + nl) * (C::CH * 16) + (((4 * i + q) ^ (nl % C::CH)) * 16) + 8 * h;
-        if (residual_dma) {
+          place[q] = slice + nl * (C::CH * 16) + (((4 * i + q) ^ (nl % C::CH)) * 16) + 8 * h;
+        if (args.residual) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const u32x2 r = *reinterpret_cast<const u32x2*>(place[q]);
@@ -574,44 +593,22 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
             z[4 * q + 2] += bf16_lo(r[1]);
             z[4 * q + 3] += bf16_hi(r[1]);
           }
-        } else if (args.residual && n < args.N) {
-          const uint16_t* r = (const uint16_t*)args.residual + (int64_t)n * args.ldr + m_wave + 32 * i + 4 * h;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (rows_full) {
-              const u32x2 v = *reinterpret_cast<const u32x2_a2*>(r + 8 * q);
-              z[4 * q] += bf16_lo(v[0]);
-              z[4 * q + 1] += bf16_hi(v[0]);
-              z[4 * q + 2] += bf16_lo(v[1]);
-              z[4 * q + 3] += bf16_hi(v[1]);
-            } else {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (m_wave + 32 * i + 8 * q + 4 * h + u < args.M)
-                  z[4 * q + u] += __uint_as_float((uint32_t)r[8 * q + u] << 16);
-            }
-          }
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<u32x2*>(place[q]) =
               (u32x2){pack_bf16(z[4 * q], z[4 * q + 1]), pack_bf16(z[4 * q + 2], z[4 * q + 3])};
       }
-      constexpr int PASSES = 32 * C::CH / 64;
-      const int m = m_wave + 8 * (lane % C::CH), left = args.M - m;
-      uint16_t* y = (uint16_t*)args.Y + (int64_t)(n_wave + 32 * j + r_t) * args.ldy + m;
+      uint16_t* y = (uint16_t*)args.Y + (int64_t)n * args.ldy + m;
       u32x4 v[PASSES];
 #pragma unroll
-      for (int t = 0; t < PASSES; ++t) {
-        const int tn = t * (64 / C::CH) + r_t;
-        v[t] = *reinterpret_cast<const u32x4*>(region + (32 * j + tn) * (C::CH * 16) + ((lane % C::CH) ^ (tn % C::CH)) * 16);
-      }
+      for (int t = 0; t < PASSES; ++t) v[t] = *reinterpret_cast<const u32x4*>(chunk(t * (64 / C::CH) + r_t));
 #pragma unroll
       for (int t = 0; t < PASSES; ++t) {
-        if (n_wave + 32 * j + t * (64 / C::CH) + r_t >= args.N) continue;
+        if (n + t * (64 / C::CH) >= args.N) continue;
         uint16_t* p = y + (int64_t)t * (64 / C::CH) * args.ldy;
         if (left >= 8) {
-          store_16b<true>(p, v[t]);
+          *reinterpret_cast<u32x4_a2*>(p) = v[t];
         } else {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
@@ -695,7 +692,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = z[8 * t + i];
-          store_row<8, true>((OutT*)args.Y + (int64_t)(n + t * TPI) * args.ldy + m, left, v);
+          store_row<8>((OutT*)args.Y + (int64_t)(n + t * TPI) * args.ldy + m, left, v);
         }
       }
     }
@@ -722,28 +719,33 @@ static p24_status launch_tile(F8Args a, hipStream_t st) {
 
 // Which kernel.  A block tile's loads per multiply shrink with its size, but a
 // launch needs enough blocks for 256 CUs: the largest tile that still gives about
-// five eighths of them wins (144 blocks for 256 x 256, whose loads are the
-// fewest; 256 x 192 where it fills one round better).  Measured, us, M x K with N tokens:
+// 144 of them wins.  Between 256 x 256 and 256 x 192 the rounds of blocks decide
+// (a round that fills every CU to the last is slower than its share: 2048 x 1024
+// with 6144 tokens, 192 blocks of 256 x 256 15.4, 256 of 256 x 192 23.6).
+// Measured, us, M x K with N tokens:
 //   8192 x 8192, 8192   256x256 264, 256x128 358, 128x128 421
 //   2304 x 768, 4096    256x192 11.8 (198 blocks), 256x256 13.2 (144), 128x128 14.3
-//   4096 x 2048, 2048   256x192 17.0 (176 blocks), 256x128 17.4 (256), 256x256 18.6 (128)
-//   2048 x 1024, 6144   256x256 15.4 (192 blocks), 256x192 23.6 (256)
-//   8192 x 4096, 1024   256x128 24.1 (256 blocks), 128x128 28.5, 256x256 28.2
-//   768 x 768, 4096     128x128 6.3 (192 blocks), 256x128 7.7, 64x64 7.3
-//   4096 x 4096, 512    128x64 12.4 (256 blocks), 128x128 14.2, 64x64 13.6
-//   4096 x 4096, 256    64x64 10.9 (256 blocks), 128x64 11.7
+//   2880 x 7232, 6098   256x192 91.7 (384 blocks), 256x256 109.7 (288)
+//   1288 x 4416, 3231   256x128 24.4 (156 blocks), 256x192 29.3 (102), 128x128 31.8
+//   768 x 768, 4096     128x128 6.3 (192 blocks), 256x128 7.7, 64x64 7.1
+//   4096 x 4096, 512    128x64 11.4 (256 blocks), 128x128 14.3, 64x64 13.4
+//   4096 x 4096, 256    64x64 9.0 (256 blocks), 128x64 10.6
 // Where one round of blocks covers the CUs at most, a block has its CU to itself:
 // two or four groups of waves then split K inside it, which keeps more loads in
-// flight (64x64 in the last line 10.9 -> 9.2; 1000 x 4032 with 517 tokens, fp32,
-// 16.7 -> 12.2; 64x32 on 4096 x 4096 with 128 tokens 9.8 -> 7.7).  A group needs a
-// few steps of its own to be worth its part in the sum: K >= 1024.
+// flight (64x64 in the last line 10.9 -> 9.2; 64x32 on 4096 x 4096 with 128 tokens
+// 9.8 -> 7.7).  A group needs a few steps of its own to be worth its part in the
+// sum: K >= 1024.
 // A tile's steps wait for memory and for each other; the kernel without shared
 // operands does neither, but reads the tokens once per 32 rows.  It wins where
 // that is little: at most 128 tiles of 32 x 32 (4096 x 4096, one token 4.9, 64x32
-// 6.2; 1024 x 8192, one token 5.7, 8.5), at most 512 with a short K (4096 x 512, 128
-// tokens 3.8, 4.0; 1000 x 1024, 400 tokens 4.9, 5.2; but 8192 x 1024, 128 tokens 7.4,
+// 6.2; 1024 x 8192, one token 5.7, 8.5), at most 640 with a short K (4096 x 512, 128
+// tokens 3.8, 4.0; 1000 x 1024, 400 tokens 4.8, 5.0; but 8192 x 1024, 128 tokens 7.6,
 // 64x64 4.9), and with few tokens (16384 x 4096, one token 8.8, 64x64 9.6; but 24
-// tokens 11.4, 64x32 10.2).
+// tokens 11.5, 64x32 10.2).  With an fp32 output every 32 x 32 tile widens its
+// operands anew, and a long K makes that the larger part (140 x 5632, 684 tokens
+// 15.5, 64x32 11.1).
+// Over 260 shapes drawn at random the choice was 1.6 % behind the fastest of the
+// eight kernels (geometric mean).
 enum class F8Kernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x192, T256x256 };
 
 static int64_t f8_blocks(const F8Args& a, int bm, int bn) {
@@ -763,17 +765,20 @@ static F8Kernel choose_f8(const F8Args& a, bool exact) {
     if (t == "256x256") return F8Kernel::T256x256;
   }
   const int64_t tiles = f8_blocks(a, 32, 32);
-  if (tiles <= 128 || a.N <= 8 || (tiles <= 512 && a.K <= 1024)) return F8Kernel::TOKENS;
+  if (a.N <= 8 || (tiles <= 640 && a.K <= 1408)) return F8Kernel::TOKENS;
+  if (tiles <= 128 && !(exact && a.N > 32 && a.K >= 3072)) return F8Kernel::TOKENS;
+  const int64_t n128 = f8_blocks(a, 256, 128);
   // the widened operands of an fp32 output do not fit the registers of the two widest
   if (!exact) {
     const int64_t n256 = f8_blocks(a, 256, 256), n192 = f8_blocks(a, 256, 192);
-    if (n256 < 160 && n192 >= 160 && n192 <= 224) return F8Kernel::T256x192;
+    const int64_t t256 = (n256 + 255) / 256 * 4, t192 = (n192 + 255) / 256 * 3;
+    if (n192 >= 160 && t192 < t256 && n192 % 256 != 0 && n192 % 256 <= 244) return F8Kernel::T256x192;
     if (n256 >= 144) return F8Kernel::T256x256;
   }
-  if (f8_blocks(a, 256, 128) >= 160) return F8Kernel::T256x128;
-  if (f8_blocks(a, 128, 128) >= 160) return F8Kernel::T128x128;
-  if (f8_blocks(a, 128, 64) >= 160) return F8Kernel::T128x64;
-  if (f8_blocks(a, 64, 64) >= 144) return F8Kernel::T64x64;
+  if ((n128 >= 144 && n128 <= 256) || n128 >= 768) return F8Kernel::T256x128;
+  if (f8_blocks(a, 128, 128) >= 144) return F8Kernel::T128x128;
+  if (f8_blocks(a, 128, 64) >= 144) return F8Kernel::T128x64;
+  if (f8_blocks(a, 64, 64) >= 128) return F8Kernel::T64x64;
   return F8Kernel::T64x32;
 }
 

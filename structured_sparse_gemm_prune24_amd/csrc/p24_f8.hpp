@@ -136,15 +136,8 @@ __device__ __forceinline__ void load_row(const T* p, int left, float (&v)[V]) {
   }
 }
 
-// NT: streamed past the L2, for outputs that are larger than it.
-template <bool NT>
-__device__ __forceinline__ void store_16b(void* p, u32x4 v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
-  else *reinterpret_cast<u32x4_a2*>(p) = v;
-}
-
 // V consecutive values to p, rounded to nearest even, `left` of them inside the row.
-template <int V, bool NT = false, typename T>
+template <int V, typename T>
 __device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V]) {
   if constexpr (sizeof(T) == 4) {
     if (left >= V) {
@@ -153,7 +146,7 @@ __device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V]) {
         u32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[4 * q + i]);
-        store_16b<NT>(p + 4 * q, w);
+        *reinterpret_cast<u32x4_a4*>(p + 4 * q) = w;
       }
     } else {
 #pragma unroll
@@ -169,7 +162,7 @@ __device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V]) {
       else w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     }
     if (left >= V) {
-      if constexpr (W == 4) store_16b<NT>(p, (u32x4){w[0], w[1], w[2], w[3]});
+      if constexpr (W == 4) *reinterpret_cast<u32x4_a2*>(p) = (u32x4){w[0], w[1], w[2], w[3]};
       else if constexpr (W == 2) *reinterpret_cast<u32x2_a1*>(p) = (u32x2){w[0], w[1]};
       else *reinterpret_cast<u32_a1*>(p) = w[0];
     } else {

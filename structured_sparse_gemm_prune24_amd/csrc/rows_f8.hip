@@ -33,7 +33,7 @@ struct RowArgs {
 template <int G>
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
+  for (int o = (G < 64 ? G : 64) / 2; o > 0; o >>= 1) {
     sum += __shfl_xor(sum, o);
     const uint32_t other = __shfl_xor(top, o);
     top = top > other ? top : other;
@@ -58,15 +58,15 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
   }
 }
 
-// G threads a row; a block of 256 threads holds four rows where G is a wave.
-template <int G> constexpr int ROW_BLOCK = G == 64 ? 256 : G;
+// G threads a row; a block of 256 threads holds several rows where G is a wave or less.
+template <int G> constexpr int ROW_BLOCK = G <= 64 ? 256 : G;
 
 template <typename T, typename OutT, int G, int E, bool NORM>
 __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
   constexpr int V = 16 / sizeof(T);   // values of a chunk: 16 bytes of input
   const int t = threadIdx.x % G;
   const int64_t row = (int64_t)blockIdx.x * (ROW_BLOCK<G> / G) + threadIdx.x / G;
-  if (row >= args.rows) return;   // whole waves, and whole blocks where G spans waves
+  if (row >= args.rows) return;   // whole groups of G threads, and whole blocks where G spans waves
   const int width = args.width;
   const T* a = (const T*)args.a + row * args.lda;
   const T* b = args.b ? (const T*)args.b + row * args.ldb : nullptr;
@@ -159,6 +159,8 @@ template <typename T, typename OutT, bool NORM>
 static p24_status rows_by_width(const RowArgs& a, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int chunks = (a.width + V - 1) / V;
+  if (chunks <= 16) return launch_rows<T, OutT, 16, 1, NORM>(a, st);
+  if (chunks <= 32) return launch_rows<T, OutT, 32, 1, NORM>(a, st);
   if (chunks <= 64) return launch_rows<T, OutT, 64, 1, NORM>(a, st);
   if (chunks <= 128) {
     if (a.rows >= 1024) return launch_rows<T, OutT, 64, 2, NORM>(a, st);   // four rows a block, no barrier
