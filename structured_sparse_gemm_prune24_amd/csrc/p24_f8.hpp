@@ -94,12 +94,13 @@ __device__ __forceinline__ void f8_act(float (&z)[N], int act) {
   }
 }
 
-// V consecutive values from p, `left` of them inside the row (the others read as
-// zero).  Any element alignment.
+// V consecutive values from p, of which [first, left) lie inside the row (the
+// others read as zero).  Any element alignment.  A part of a chunk is loaded value
+// by value at clamped places, all on the way at once.
 template <int V, typename T>
-__device__ __forceinline__ void load_row(const T* p, int left, float (&v)[V]) {
+__device__ __forceinline__ void load_row(const T* p, int left, float (&v)[V], int first = 0) {
   static_assert(V % 4 == 0 && (sizeof(T) == 4 || V == 8 || V == 4), "whole vectors");
-  if (left >= V) {
+  if (first <= 0 && left >= V) {
     if constexpr (sizeof(T) == 2) {
       uint32_t w[V / 2];
       if constexpr (V == 8) {
@@ -126,21 +127,27 @@ __device__ __forceinline__ void load_row(const T* p, int left, float (&v)[V]) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] = 0.0f;
-      if (i < left) {
-        if constexpr (sizeof(T) == 2) v[i] = __uint_as_float((uint32_t)p[i] << 16);
-        else v[i] = p[i];
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    if (left > 0 && first < V) {
+      T x[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = p[min(max(i, first), left - 1)];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float f;
+        if constexpr (sizeof(T) == 2) f = __uint_as_float((uint32_t)x[i] << 16);
+        else f = x[i];
+        v[i] = i >= first && i < left ? f : 0.0f;
       }
     }
   }
 }
 
-// V consecutive values to p, rounded to nearest even, `left` of them inside the row.
+// V consecutive values to p, rounded to nearest even, [first, left) of them inside the row.
 template <int V, typename T>
-__device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V]) {
+__device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V], int first = 0) {
   if constexpr (sizeof(T) == 4) {
-    if (left >= V) {
+    if (first <= 0 && left >= V) {
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
         u32x4 w;
@@ -151,7 +158,7 @@ __device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V]) {
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i < left) p[i] = v[i];
+        if (i >= first && i < left) p[i] = v[i];
     }
   } else {
     constexpr int PER = 4 / sizeof(T), W = V / PER;    // values per word, words
@@ -161,14 +168,14 @@ __device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V]) {
       if constexpr (sizeof(T) == 1) w[i] = pack_f8(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       else w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     }
-    if (left >= V) {
+    if (first <= 0 && left >= V) {
       if constexpr (W == 4) *reinterpret_cast<u32x4_a2*>(p) = (u32x4){w[0], w[1], w[2], w[3]};
       else if constexpr (W == 2) *reinterpret_cast<u32x2_a1*>(p) = (u32x2){w[0], w[1]};
       else *reinterpret_cast<u32_a1*>(p) = w[0];
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i < left) {
+        if (i >= first && i < left) {
           const uint32_t x = w[i / PER] >> (8 * sizeof(T) * (i % PER));
           if constexpr (sizeof(T) == 1) p[i].v = (uint8_t)x;
           else p[i] = (uint16_t)x;

@@ -24,66 +24,81 @@ struct RowArgs {
   void* y;
   float* scale;         // 8-bit output
   int64_t lda, ldb, ldh, ldy;
+  int64_t ref, ldref;   // place of row 0 of the tensor whose chunks are aligned, in elements, and its leading dimension
+  int shift;            // bf16 rows off the 16-byte grid: chunks start on it, the first and last are parts
   int rows, width;
   float eps;
+  int threads;          // of a block, where a row has one to itself
   int act;
 };
 
-// Sum and magnitude maximum over the G threads of a row, the same in each.
+// Sum and magnitude maximum over the threads of a row, the same in each: G lanes
+// of a wave, or (G = 0) the whole block.
 template <int G>
-__device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
+__device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int threads) {
 #pragma unroll
-  for (int o = (G < 64 ? G : 64) / 2; o > 0; o >>= 1) {
+  for (int o = (G ? G : 64) / 2; o > 0; o >>= 1) {
     sum += __shfl_xor(sum, o);
     const uint32_t other = __shfl_xor(top, o);
     top = top > other ? top : other;
   }
-  if constexpr (G > 64) {
-    constexpr int W = G / 64;
-    __shared__ float sums[W];
-    __shared__ uint32_t tops[W];
-    const int wave = threadIdx.x >> 6;
+  if constexpr (G == 0) {
+    constexpr int MAX_WAVES = 16;
+    __shared__ __attribute__((aligned(16))) float sums[MAX_WAVES];
+    __shared__ __attribute__((aligned(16))) uint32_t tops[MAX_WAVES];
+    const int wave = threadIdx.x >> 6, waves = threads >> 6;
     if ((threadIdx.x & 63) == 0) {
       sums[wave] = sum;
       tops[wave] = top;
     }
     __syncthreads();
+    // all entries are read at once; those past the block's waves are dropped
+    float s[MAX_WAVES];
+    uint32_t m[MAX_WAVES];
+#pragma unroll
+    for (int i = 0; i < MAX_WAVES; ++i) {
+      s[i] = sums[i];
+      m[i] = tops[i];
+    }
     sum = 0.0f;
     top = 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      sum += sums[i];
-      top = top > tops[i] ? top : tops[i];
+    for (int i = 0; i < MAX_WAVES; ++i) {
+      sum += i < waves ? s[i] : 0.0f;
+      top = max(top, i < waves ? m[i] : 0u);
     }
   }
 }
 
-// G threads a row; a block of 256 threads holds several rows where G is a wave or less.
-template <int G> constexpr int ROW_BLOCK = G <= 64 ? 256 : G;
-
+// G lanes a row, several rows to a block of 256 threads; G = 0: a block a row.
 template <typename T, typename OutT, int G, int E, bool NORM>
-__global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
+__global__ __launch_bounds__(G ? 256 : 1024) void k_rows(const RowArgs args) {
   constexpr int V = 16 / sizeof(T);   // values of a chunk: 16 bytes of input
-  const int t = threadIdx.x % G;
-  const int64_t row = (int64_t)blockIdx.x * (ROW_BLOCK<G> / G) + threadIdx.x / G;
-  if (row >= args.rows) return;   // whole groups of G threads, and whole blocks where G spans waves
+  const int t = G ? threadIdx.x % (G ? G : 1) : threadIdx.x, threads = G ? G : args.threads;
+  const int64_t row = G ? (int64_t)blockIdx.x * (256 / (G ? G : 1)) + threadIdx.x / (G ? G : 1) : blockIdx.x;
+  if (row >= args.rows) return;   // whole groups of G lanes
   const int width = args.width;
   const T* a = (const T*)args.a + row * args.lda;
   const T* b = args.b ? (const T*)args.b + row * args.ldb : nullptr;
 
+  // chunk k of the row is its values [k V - d, k V - d + V)
+  int d = 0;
+  if constexpr (sizeof(T) == 2)
+    if (args.shift) d = (int)((args.ref + row * args.ldref) % V);
+
   float v[E][V], u[E][V], w[NORM ? E : 1][V];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int c = (t + e * G) * V;
-    load_row<V>(a + c, width - c, v[e]);
-    if (b) load_row<V>(b + c, width - c, u[e]);
+    const int c = (t + e * threads) * V - d;
+    load_row<V>(a + c, width - c, v[e], -c);
+    if (b) load_row<V>(b + c, width - c, u[e], -c);
   }
   // the weights are asked for ahead of the sum's store, which the compiler must keep in its place
   if constexpr (NORM) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int c = (t + e * G) * V;
-      load_row<V>(args.weight + c, width - c, w[e]);
+      const int c = (t + e * threads) * V - d;
+      load_row<V>(args.weight + c, width - c, w[e], -c);
     }
   }
   if constexpr (!NORM) {
@@ -93,10 +108,10 @@ __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
   if (b) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int c = (t + e * G) * V;
+      const int c = (t + e * threads) * V - d;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[e][i] = NORM ? v[e][i] + u[e][i] : v[e][i] * u[e][i];
-      if constexpr (NORM) store_row<V>((T*)args.h + row * args.ldh + c, width - c, v[e]);
+      if constexpr (NORM) store_row<V>((T*)args.h + row * args.ldh + c, width - c, v[e], -c);
     }
   }
   // values past the row are zero: act(0) = 0 for every activation
@@ -119,7 +134,7 @@ __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
   // two factors, not their product: with a tiny scale the product overflows
   float k = 1.0f, inv = 1.0f;
   if constexpr (NORM || sizeof(OutT) == 1) {
-    row_reduce<G>(sum, top);
+    row_reduce<G>(sum, top, threads);
     if constexpr (NORM) k = 1.0f / sqrtf(sum / (float)width + args.eps);
     if constexpr (sizeof(OutT) == 1) {
       const float s = f8_scale(__uint_as_float(top) * k);
@@ -130,53 +145,59 @@ __global__ __launch_bounds__(ROW_BLOCK<G>) void k_rows(const RowArgs args) {
   OutT* y = (OutT*)args.y + row * args.ldy;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int c = (t + e * G) * V;
+    const int c = (t + e * threads) * V - d;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if constexpr (NORM) v[e][i] *= k;
       if constexpr (sizeof(OutT) == 1) v[e][i] *= inv;
     }
-    store_row<V>(y + c, width - c, v[e]);
+    store_row<V>(y + c, width - c, v[e], -c);
   }
 }
 
 template <typename T, typename OutT, int G, int E, bool NORM>
-static p24_status launch_rows(const RowArgs& a, hipStream_t st) {
-  constexpr int R = ROW_BLOCK<G> / G;
-  hipLaunchKernelGGL((k_rows<T, OutT, G, E, NORM>), dim3((unsigned)(((int64_t)a.rows + R - 1) / R)), dim3(ROW_BLOCK<G>), 0, st, a);
+static p24_status launch_rows(RowArgs a, int chunks, hipStream_t st) {
+  const int per = G ? 256 / (G ? G : 1) : 1;                                       // rows of a block
+  const int threads = G ? 256 : ((chunks + E - 1) / E + 63) / 64 * 64;
+  a.threads = threads;
+  hipLaunchKernelGGL((k_rows<T, OutT, G, E, NORM>), dim3((unsigned)((a.rows + (int64_t)per - 1) / per)), dim3(threads), 0,
+                     st, a);
   return launch_status();
 }
 
-// Threads and chunks of a row, by its count of 16-byte chunks: as few chunks a
-// thread as a block of 512 or 1024 allows, because a row's time is its trips to
-// memory and the reduction.  Measured, us (bf16 unless said):
+// Threads and chunks of a row, by its count of 16-byte chunks: whole waves, as few
+// chunks a thread as blocks of up to ten waves allow, because a row's time is its
+// trips to memory and the reduction; several rows to a block where one needs a
+// wave or less.  Measured, us (bf16 unless said):
 //   norm 8192 x 8192   512 x 2 89.4 (5.3 TB/s), 256 x 4 100.7, 1024 x 1 89.2
 //   gate 4096 x 8192   512 x 2 31.6 (5.3 TB/s), 256 x 4 35.8, 1024 x 1 34.5
-//   norm 4096 x 4096 fp32   1024 x 1 39.8, 512 x 2 41.9;  gate 777 x 2051 fp32  6.0, 6.5
 //   gate 2000 x 4096   512 x 1 9.6, 256 x 2 10.2;  norm 1 x 4096  3.3, 3.5
 //   norm 8192 x 1024   64 x 2 12.4, 128 x 1 13.8, 256 x 1 15.7;  norm 2 x 700  128 x 1 3.8, 64 x 2 4.3
+//   gate 6526 x 140    32 lanes 5.1, 64 lanes 7.0;  gate 777 x 2051 fp32  576 x 1 4.9, 1024 x 1 5.7
+// bf16 rows that do not all start on 16 bytes take their chunks on that grid, at
+// the price of a part of a chunk at either end: loads and above all stores across
+// it cost more (norm 8192 x 4095, bf16 out: 67 us, 83 on the row's own grid, 47 for
+// 4096).
 template <typename T, typename OutT, bool NORM>
-static p24_status rows_by_width(const RowArgs& a, hipStream_t st) {
+static p24_status rows_by_width(RowArgs a, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const int chunks = (a.width + V - 1) / V;
-  if (chunks <= 16) return launch_rows<T, OutT, 16, 1, NORM>(a, st);
-  if (chunks <= 32) return launch_rows<T, OutT, 32, 1, NORM>(a, st);
-  if (chunks <= 64) return launch_rows<T, OutT, 64, 1, NORM>(a, st);
-  if (chunks <= 128) {
-    if (a.rows >= 1024) return launch_rows<T, OutT, 64, 2, NORM>(a, st);   // four rows a block, no barrier
-    return launch_rows<T, OutT, 128, 1, NORM>(a, st);
+  if constexpr (sizeof(T) == 2) {
+    // the sum's rows where there is one, else the output's, else the input's
+    const void* ref = NORM && a.h ? a.h : sizeof(OutT) == 2 ? a.y : a.a;
+    a.ldref = NORM && a.h ? a.ldh : sizeof(OutT) == 2 ? a.ldy : a.lda;
+    a.ref = (int64_t)((uintptr_t)ref / sizeof(T) % V);
+    a.shift = a.ref != 0 || a.ldref % V != 0;
   }
-  if (chunks <= 256) return launch_rows<T, OutT, 256, 1, NORM>(a, st);
-  if (chunks <= 512) return launch_rows<T, OutT, 512, 1, NORM>(a, st);
-  if (chunks <= 1024) {
-    if constexpr (sizeof(T) == 4) return launch_rows<T, OutT, 1024, 1, NORM>(a, st);
-    else return launch_rows<T, OutT, 512, 2, NORM>(a, st);
-  }
-  if (chunks <= 2048) return launch_rows<T, OutT, 1024, 2, NORM>(a, st);
-  if (chunks <= 4096) return launch_rows<T, OutT, 1024, 4, NORM>(a, st);
-  if (chunks <= 8192) return launch_rows<T, OutT, 1024, 8, NORM>(a, st);
-  if constexpr (sizeof(T) == 4) return launch_rows<T, OutT, 1024, 16, NORM>(a, st);
-  else return P24_ERR_SHAPE;
+  const int chunks = (a.width + V - 1 + (a.shift ? V - 1 : 0)) / V;
+  if (chunks <= 16) return launch_rows<T, OutT, 16, 1, NORM>(a, chunks, st);
+  if (chunks <= 32) return launch_rows<T, OutT, 32, 1, NORM>(a, chunks, st);
+  if (chunks <= 64) return launch_rows<T, OutT, 64, 1, NORM>(a, chunks, st);
+  if (chunks <= 128 && a.rows >= 1024) return launch_rows<T, OutT, 64, 2, NORM>(a, chunks, st);   // no barrier
+  if (chunks <= 640 || (sizeof(T) == 4 && chunks <= 1024)) return launch_rows<T, OutT, 0, 1, NORM>(a, chunks, st);
+  if (chunks <= 2048) return launch_rows<T, OutT, 0, 2, NORM>(a, chunks, st);
+  if (chunks <= 4096) return launch_rows<T, OutT, 0, 4, NORM>(a, chunks, st);
+  if (chunks <= 8192) return launch_rows<T, OutT, 0, 8, NORM>(a, chunks, st);
+  return launch_rows<T, OutT, 0, 17, NORM>(a, chunks, st);
 }
 
 template <bool NORM>

@@ -49,7 +49,8 @@ def _check_rows(got, y, rel, out):
 
 NORM_SHAPES = [(1, 1, 0), (1, 64, 0), (3, 7, 2), (5, 511, 1), (4, 512, 0), (2, 513, 3), (7, 1003, 5), (2, 2048, 0),
                (3, 2049, 7), (1, 4096, 0), (9, 4097, 0), (2, 8192, 8), (2, 8193, 0), (1, 16385, 1), (2, 40001, 3),
-               (1, 65536, 0), (300, 128, 0), (1025, 260, 4)]
+               (1, 65536, 0), (2, 65536, 1), (300, 128, 0), (1025, 260, 4), (1030, 700, 1), (5, 120, 1), (9, 250, 1),
+               (3, 4095, 0), (2, 5121, 2), (2, 9000, 1)]
 
 
 @pytest.mark.parametrize("out", [F8, torch.bfloat16, torch.float32], ids=["f8", "bf16", "f32"])
