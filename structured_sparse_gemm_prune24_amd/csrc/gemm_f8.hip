@@ -30,6 +30,7 @@ struct F8Args {
   int M, N, K;
   int act;
   int nbm, nbn;   // grid of block tiles
+  int stream;     // the output's rows are whole cache lines (bf16)
   int res_dma;    // the residual is whole aligned 16 B chunks: it can go straight to LDS
 };
 
@@ -270,6 +271,13 @@ __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, void* dst
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// 16 bytes per lane to the buffer at voff, past the L2 (nt).  Only as a buffer
+// store: the compiler merges a non-temporal store through a pointer with the plain
+// one of the other branch.
+__device__ __forceinline__ void stream_16b(__amdgpu_buffer_rsrc_t r, u32x4 v, uint32_t voff) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 2);
 }
 
 template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
@@ -532,35 +540,40 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     uint8_t* region = lds_all + (count + wave / C::RPS) % NSTAGE * C::STAGE + wave % C::RPS * C::REGION;
     const int m_wave = m0 + wm * C::WTM, n_wave = n0 + wn * C::WTN;
     const int m = m_wave + 8 * (lane % C::CH), left = args.M - m;     // a lane's features of a whole row
-    constexpr int PASSES = 32 * C::CH / 64;
+    constexpr int TPP = 64 / C::CH, PASSES = 32 / TPP;                  // tokens a pass, passes a slice
+    // Rows of whole cache lines stream past the L2, which would only flush them
+    // (8192^3 277 -> 263 us, 2304 x 768 with 4096 tokens 13.0 -> 10.7); parts of
+    // lines are joined there (7023 x 192 with 5744 tokens 36 us, 49 streamed).
+    const __amdgpu_buffer_rsrc_t y_rsrc =
+        f8_rsrc((const uint8_t*)args.Y + ((int64_t)n_wave * args.ldy + m_wave) * 2, 0xFFFFFFFFu);
+    // a lane's 16 B of the region's token t
+    auto chunk = [&](int t) { return region + t * (C::CH * 16) + ((lane % C::CH) ^ (t % C::CH)) * 16; };
+    if (args.residual && !residual_dma) {
+      // rows at any alignment come through registers, four passes at a time
+#pragma unroll 1
+      for (int t0 = r_t; t0 < C::WTN; t0 += 4 * TPP) {
+        u32x4 r[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int n = n_wave + t0 + t * TPP;
+          const uint16_t* p = (const uint16_t*)args.residual + (int64_t)n * args.ldr + m;
+          r[t] = (u32x4){0, 0, 0, 0};
+          if (n < args.N && left >= 8) {
+            r[t] = *reinterpret_cast<const u32x4_a2*>(p);
+          } else if (n < args.N) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (u < left) r[t][u / 2] |= (uint32_t)p[u] << (16 * (u & 1));
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (t0 + t * TPP < C::WTN) *reinterpret_cast<u32x4*>(chunk(t0 + t * TPP)) = r[t];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const float sx = sc[2 * BM + wn * C::WTN + 32 * j + nl];
-      uint8_t* slice = region + 32 * j * (C::CH * 16);
-      const int n = n_wave + 32 * j + r_t;                              // a lane's first token of the slice
-      auto chunk = [&](int t) { return slice + t * (C::CH * 16) + ((lane % C::CH) ^ (t % C::CH)) * 16; };
-      if (args.residual && !residual_dma) {     // rows at any alignment come through registers
-        constexpr int B = PASSES < 4 ? PASSES : 4;
-#pragma unroll 1
-        for (int t0 = 0; t0 < PASSES; t0 += B) {
-          u32x4 r[B];
-#pragma unroll
-          for (int t = 0; t < B; ++t) {
-            const int step = (t0 + t) * (64 / C::CH);
-            const uint16_t* p = (const uint16_t*)args.residual + (int64_t)(n + step) * args.ldr + m;
-            r[t] = (u32x4){0, 0, 0, 0};
-            if (n + step < args.N && left >= 8) {
-              r[t] = *reinterpret_cast<const u32x4_a2*>(p);
-            } else if (n + step < args.N) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                if (u < left) r[t][u / 2] |= (uint32_t)p[u] << (16 * (u & 1));
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < B; ++t) *reinterpret_cast<u32x4*>(chunk((t0 + t) * (64 / C::CH) + r_t)) = r[t];
-        }
-      }
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         float z[16];
@@ -583,7 +596,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
         uint8_t* place[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          place[q] = slice + nl * (C::CH * 16) + (((4 * i + q) ^ (nl % C::CH)) * 16) + 8 * h;
+          place[q] = region + (32 * j + nl) * (C::CH * 16) + (((4 * i + q) ^ (nl % C::CH)) * 16) + 8 * h;
         if (args.residual) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -599,16 +612,17 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
           *reinterpret_cast<u32x2*>(place[q]) =
               (u32x2){pack_bf16(z[4 * q], z[4 * q + 1]), pack_bf16(z[4 * q + 2], z[4 * q + 3])};
       }
-      uint16_t* y = (uint16_t*)args.Y + (int64_t)n * args.ldy + m;
       u32x4 v[PASSES];
 #pragma unroll
-      for (int t = 0; t < PASSES; ++t) v[t] = *reinterpret_cast<const u32x4*>(chunk(t * (64 / C::CH) + r_t));
+      for (int t = 0; t < PASSES; ++t) v[t] = *reinterpret_cast<const u32x4*>(chunk(32 * j + t * TPP + r_t));
 #pragma unroll
       for (int t = 0; t < PASSES; ++t) {
-        if (n + t * (64 / C::CH) >= args.N) continue;
-        uint16_t* p = y + (int64_t)t * (64 / C::CH) * args.ldy;
+        const int n = n_wave + 32 * j + t * TPP + r_t;
+        if (n >= args.N) continue;
+        uint16_t* p = (uint16_t*)args.Y + (int64_t)n * args.ldy + m;
         if (left >= 8) {
-          *reinterpret_cast<u32x4_a2*>(p) = v[t];
+          if (args.stream) stream_16b(y_rsrc, v[t], (uint32_t)((32 * j + t * TPP + r_t) * args.ldy + 8 * (lane % C::CH)) * 2);
+          else *reinterpret_cast<u32x4_a2*>(p) = v[t];
         } else {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
@@ -692,7 +706,8 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = z[8 * t + i];
-          store_row<8>((OutT*)args.Y + (int64_t)(n + t * TPI) * args.ldy + m, left, v);
+          OutT* y = (OutT*)args.Y + (int64_t)(n + t * TPI) * args.ldy + m;
+          store_row<8>(y, left, v);
         }
       }
     }
@@ -861,6 +876,7 @@ extern "C" P24_API p24_status spmm24_f8(const void* data, const float* w_scale, 
   a.N = (int)N;
   a.K = (int)K;
   a.act = act;
+  a.stream = aligned(Y, 128) && ldy * (int64_t)ye % 128 == 0 && (uint64_t)ldy * 1024 < (1ull << 32);
   a.res_dma = residual && aligned(residual, 16) && ldr % 8 == 0 && M % 8 == 0 && (uint64_t)ldr * 1024 < (1ull << 32);
   if (y_dtype == P24_F32) return launch_f8<float>(a, (hipStream_t)stream);
   return launch_f8<uint16_t>(a, (hipStream_t)stream);
