@@ -255,10 +255,6 @@ struct F8Frags {
   }
 };
 
-// Buffer over [base, base + bytes): loads past it return zero.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_rsrc(const uint8_t* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, (int)bytes, 0x00020000);
-}
 // 16 bytes per lane from voff + soff straight to LDS, lane l at dst + 16 l.
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, soff, 0, 0);
@@ -271,13 +267,6 @@ __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, void* dst
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// 16 bytes per lane to the buffer at voff, past the L2 (nt).  Only as a buffer
-// store: the compiler merges a non-temporal store through a pointer with the plain
-// one of the other branch.
-__device__ __forceinline__ void stream_16b(__amdgpu_buffer_rsrc_t r, u32x4 v, uint32_t voff) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 2);
 }
 
 template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>

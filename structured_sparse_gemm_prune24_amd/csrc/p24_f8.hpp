@@ -143,6 +143,17 @@ __device__ __forceinline__ void load_row(const T* p, int left, float (&v)[V], in
   }
 }
 
+// Buffer over [base, base + bytes): loads past it return zero.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_rsrc(const uint8_t* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, (int)bytes, 0x00020000);
+}
+// 16 bytes per lane to the buffer at voff, past the L2 (nt).  Only as a buffer
+// store: the compiler merges a non-temporal store through a pointer with the plain
+// one of the other branch.
+__device__ __forceinline__ void stream_16b(__amdgpu_buffer_rsrc_t r, u32x4 v, uint32_t voff) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 2);
+}
+
 // V consecutive values to p, rounded to nearest even, [first, left) of them inside the row.
 template <int V, typename T>
 __device__ __forceinline__ void store_row(T* p, int left, const float (&v)[V], int first = 0) {
