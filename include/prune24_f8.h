@@ -52,6 +52,7 @@ enum { P24_ACT_SILU = 3 };    /* z / (1 + exp(-z)), next to P24_ACT_NONE, _RELU,
  *             and leading dimension); y is computed from the unrounded sum.
  *   y         output, y_dtype P24_F8, P24_BF16 or P24_F32, leading dimension ldy.
  *   scale     output, one fp32 per token, with P24_F8; NULL otherwise.
+ *   y and scale overlap no input and not h.
  *   1 <= width <= P24_ROW_MAX; tokens < 2^22 (else
  *   P24_ERR_UNSUPPORTED); tokens == 0 is a no-op.
  *   eps >= 0 and finite.
@@ -119,8 +120,6 @@ P24_API p24_status prune24_decompress_f8(const void* data, const float* scale, i
  *   act       P24_ACT_NONE, _RELU, _GELU or _SILU (as for gated_act).
  *   residual  as Y, leading dimension ldr, or NULL.  It may be Y itself (same
  *             pointer and leading dimension); otherwise Y overlaps no input.
- *   workspace device scratch, spmm24_f8_workspace_bytes(M, K, N) bytes, 16 B
- *             aligned, contents on entry do not matter; NULL where that is 0.
  * The kernel is picked from the shape.  The environment variable
  * P24_F8_TILE=tokens|64x32|64x64|128x64|128x128|256x128|256x192|256x256, read at
  * each call, forces one (a measurement and test aid; results stay within the
@@ -130,12 +129,10 @@ P24_API p24_status prune24_decompress_f8(const void* data, const float* scale, i
  * cut toward zero to 2^-13 of the exponent of the largest of the eight, and
  * those sums in fp32; that is below the output's own rounding.
  */
-P24_API size_t spmm24_f8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 P24_API p24_status spmm24_f8(const void* data, const float* w_scale, int64_t M, int64_t K,
                              const void* X, int64_t ldx, const float* x_scale, int64_t N, void* Y,
                              int32_t y_dtype, int64_t ldy, const float* bias, int32_t act,
-                             const void* residual, int64_t ldr, void* workspace, size_t ws_bytes,
-                             void* stream);
+                             const void* residual, int64_t ldr, void* stream);
 
 #ifdef __cplusplus
 }

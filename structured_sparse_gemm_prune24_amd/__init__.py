@@ -122,9 +122,8 @@ _F8_SIGNATURES = {
     "prune24_f8_bytes": (_c_size, [_c_i64, _c_i64]),
     "prune24_compress_f8": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
     "prune24_decompress_f8": (_c_i32, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp]),
-    "spmm24_f8_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
     "spmm24_f8": (_c_i32, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i32, _c_i64, _c_vp,
-                           _c_i32, _c_vp, _c_i64, _c_vp, _c_size, _c_vp]),
+                           _c_i32, _c_vp, _c_i64, _c_vp]),
 }
 
 _LIB = None

@@ -24,7 +24,6 @@ namespace {
 decltype(&rms_norm) p_norm = nullptr;
 decltype(&gated_act) p_gate = nullptr;
 decltype(&spmm24_f8) p_product = nullptr;
-decltype(&spmm24_f8_workspace_bytes) p_workspace = nullptr;
 
 constexpr at::ScalarType F8 = at::kFloat8_e4m3fn;
 
@@ -169,37 +168,37 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Device dev = x->device();
     const float *ws = vec(a[1], M, dev), *xs = vec(a[5], N, dev), *bias = nullptr;
     if (!ws || !xs || data.device() != dev || x->size(1) != K || M < 1) return none();
+    if (data.scalar_type() != at::kByte || !data.is_contiguous() ||
+        data.numel() < (M + 127) / 128 * ((K + 127) / 128) * 2 * 5120)
+      return none();
     if (!is_none(a[7]) && !(bias = vec(a[7], M, dev))) return none();
     const long code = PyLong_AsLong(a[6]), act = PyLong_AsLong(a[8]);
     if (!is_none(a[9]) && (!rows(a[9], r, ldr) || r->scalar_type() != type_of((int)code) || r->device() != dev ||
                            r->size(0) != N || r->size(1) != M))
       return none();
-    at::Tensor y = make({N, M}, type_of((int)code), dev), scratch;
-    const size_t need = p_workspace(M, K, N);
-    if (need) scratch = make({(int64_t)need}, at::kByte, dev);
+    at::Tensor y = make({N, M}, type_of((int)code), dev);
     const p24_status st =
         p_product(data.data_ptr(), ws, M, K, x->data_ptr(), ldx, xs, N, y.data_ptr(), (int)code, M, bias, (int)act,
-                  r ? r->data_ptr() : nullptr, ldr, need ? scratch.data_ptr() : nullptr, need, stream_of(dev));
+                  r ? r->data_ptr() : nullptr, ldr, stream_of(dev));
     if (st != P24_OK) return none();
     return THPVariable_Wrap(y);
   });
 }
 
-// bind(rms_norm, gated_act, spmm24_f8, spmm24_f8_workspace_bytes): their addresses
+// bind(rms_norm, gated_act, spmm24_f8): their addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "bind takes three addresses");
     return nullptr;
   }
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  void* p[3];
+  for (int i = 0; i < 3; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
   p_norm = reinterpret_cast<decltype(p_norm)>(p[0]);
   p_gate = reinterpret_cast<decltype(p_gate)>(p[1]);
   p_product = reinterpret_cast<decltype(p_product)>(p[2]);
-  p_workspace = reinterpret_cast<decltype(p_workspace)>(p[3]);
   Py_RETURN_NONE;
 }
 

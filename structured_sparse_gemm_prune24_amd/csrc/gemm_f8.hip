@@ -10,7 +10,7 @@
 // 8 (i / 4) + 4 (L / 32) + i % 4, i = 0..15: four consecutive features of one
 // token at a time, which is the output's own order.
 #include <cstdlib>
-#include <string>
+#include <cstring>
 #include <type_traits>
 
 #include "p24_api_internal.hpp"
@@ -716,6 +716,7 @@ template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
 static p24_status launch_tile(F8Args a, hipStream_t st) {
   a.nbm = (a.M + BM - 1) / BM;
   a.nbn = (a.N + BN - 1) / BN;
+  if ((int64_t)a.nbm * a.nbn * (WGM * WGN * KG * 64) > UINT32_MAX) return P24_ERR_UNSUPPORTED;   // a grid's threads
   hipLaunchKernelGGL((k_gemm_f8<BM, BN, WGM, WGN, LW, KG, OutT>), dim3((unsigned)(a.nbm * a.nbn)),
                      dim3(WGM * WGN * KG * 64), 0, st, a);
   return launch_status();
@@ -758,15 +759,15 @@ static int64_t f8_blocks(const F8Args& a, int bm, int bn) {
 
 static F8Kernel choose_f8(const F8Args& a, bool exact) {
   if (const char* e = getenv("P24_F8_TILE")) {
-    const std::string t(e);
-    if (t == "tokens") return F8Kernel::TOKENS;
-    if (t == "64x32") return F8Kernel::T64x32;
-    if (t == "64x64") return F8Kernel::T64x64;
-    if (t == "128x64") return F8Kernel::T128x64;
-    if (t == "128x128") return F8Kernel::T128x128;
-    if (t == "256x128" || (exact && (t == "256x192" || t == "256x256"))) return F8Kernel::T256x128;
-    if (t == "256x192") return F8Kernel::T256x192;
-    if (t == "256x256") return F8Kernel::T256x256;
+    auto is = [&](const char* name) { return strcmp(e, name) == 0; };
+    if (is("tokens")) return F8Kernel::TOKENS;
+    if (is("64x32")) return F8Kernel::T64x32;
+    if (is("64x64")) return F8Kernel::T64x64;
+    if (is("128x64")) return F8Kernel::T128x64;
+    if (is("128x128")) return F8Kernel::T128x128;
+    if (is("256x128") || (exact && (is("256x192") || is("256x256")))) return F8Kernel::T256x128;
+    if (is("256x192")) return F8Kernel::T256x192;
+    if (is("256x256")) return F8Kernel::T256x256;
   }
   const int64_t tiles = f8_blocks(a, 32, 32);
   if (a.N <= 8 || (tiles <= 640 && a.K <= 1408)) return F8Kernel::TOKENS;
@@ -824,17 +825,10 @@ static p24_status launch_f8(const F8Args& a, hipStream_t st) {
 
 using namespace p24;
 
-extern "C" P24_API size_t spmm24_f8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  (void)M;
-  (void)K;
-  (void)N;
-  return 0;
-}
-
 extern "C" P24_API p24_status spmm24_f8(const void* data, const float* w_scale, int64_t M, int64_t K, const void* X,
                                         int64_t ldx, const float* x_scale, int64_t N, void* Y, int32_t y_dtype,
                                         int64_t ldy, const float* bias, int32_t act, const void* residual, int64_t ldr,
-                                        void* workspace, size_t ws_bytes, void* stream) {
+                                        void* stream) {
   if (y_dtype != P24_F32 && y_dtype != P24_BF16) return P24_ERR_DTYPE;
   if (!f8_act_known(act)) return P24_ERR_UNSUPPORTED;
   if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return P24_ERR_SHAPE;
@@ -847,9 +841,6 @@ extern "C" P24_API p24_status spmm24_f8(const void* data, const float* w_scale, 
   if (!aligned(data, 16) || !aligned(X, 16) || ldx % 16 || !aligned(Y, ye) || (residual && !aligned(residual, ye)) ||
       !aligned(w_scale, 4) || !aligned(x_scale, 4) || (bias && !aligned(bias, 4)))
     return P24_ERR_ALIGN;
-  const size_t need = spmm24_f8_workspace_bytes(M, K, N);
-  if (need && (!workspace || ws_bytes < need)) return P24_ERR_WORKSPACE;
-  if (need && !aligned(workspace, 16)) return P24_ERR_ALIGN;
   F8Args a{};
   a.W = (const uint8_t*)data;
   a.w_scale = w_scale;

@@ -59,7 +59,7 @@ def _call():
             raise RuntimeError("_f8_call.so is missing: build it with __graft_entry__.build() "
                                "or python structured_sparse_gemm_prune24_amd/build.py") from e
         c.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                 for f in (L.rms_norm, L.gated_act, L.spmm24_f8, L.spmm24_f8_workspace_bytes)))
+                 for f in (L.rms_norm, L.gated_act, L.spmm24_f8)))
         _CALL = c
     return _CALL
 
@@ -196,9 +196,20 @@ def compress_f8(W) -> Compressed24F8:
     return Compressed24F8(data, scale, M, K)
 
 
+def _weight(c: Compressed24F8, dev):
+    """Pointer of a compressed weight's scales, after checking its buffers."""
+    d = c.data
+    if not d.is_cuda or d.device != dev:
+        raise ValueError(f"the weight is on {d.device}, the operation runs on {dev}")
+    if d.dtype is not torch.uint8 or not d.is_contiguous() or d.numel() < lib().prune24_f8_bytes(c.M, c.K):
+        raise ValueError(f"the weight's data is not the compressed form of {(c.M, c.K)}")
+    return _vector(c.scale, "the weight's scale", c.M, dev)
+
+
 def decompress_f8(c: Compressed24F8):
     """Dense fp32 [M, K]: value times scale at the kept positions, zeros elsewhere."""
     dev = c.data.device
+    _weight(c, dev)
     out = torch.empty((c.M, c.K), dtype=torch.float32, device=dev)
     _check(lib().prune24_decompress_f8(c.data.data_ptr(), c.scale.data_ptr(), c.M, c.K, out.data_ptr(), c.K,
                                        torch.cuda.current_stream(dev).cuda_stream), "prune24_decompress_f8")
@@ -223,8 +234,7 @@ def spmm24_f8(c: Compressed24F8, X: Quantized8, out_dtype=torch.bfloat16, out=No
     N, K = v.shape
     if K != c.K:
         raise ValueError(f"X has {K} features, W has K = {c.K}")
-    if c.data.device != dev:
-        raise ValueError(f"the weight is on {c.data.device}, the operation runs on {dev}")
+    ws = _weight(c, dev)
     xs = _vector(X.scale, "X.scale", N, dev)
     bp = None if bias is None else _vector(bias, "bias", c.M, dev)
     a = _act_code(act)
@@ -240,12 +250,8 @@ def spmm24_f8(c: Compressed24F8, X: Quantized8, out_dtype=torch.bfloat16, out=No
     if residual is not None:
         ldr = _rows(residual, "residual", dev, (out.dtype,), shape)
         rp = residual.data_ptr()
-    L = lib()
-    need = L.spmm24_f8_workspace_bytes(c.M, K, N)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _check(L.spmm24_f8(c.data.data_ptr(), c.scale.data_ptr(), c.M, K, v.data_ptr(), ldx, xs, N, out.data_ptr(),
-                       _CODES[out.dtype], ldy, bp, a, rp, ldr, ws.data_ptr() if need else None, need,
-                       torch.cuda.current_stream(dev).cuda_stream), "spmm24_f8")
+    _check(lib().spmm24_f8(c.data.data_ptr(), ws, c.M, K, v.data_ptr(), ldx, xs, N, out.data_ptr(),
+                           _CODES[out.dtype], ldy, bp, a, rp, ldr, torch.cuda.current_stream(dev).cuda_stream), "spmm24_f8")
     return out
 
 

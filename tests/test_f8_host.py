@@ -9,8 +9,8 @@ from f8_ref import F8, compress, decompress, f8_values, pack, smfmac64_model
 
 torch = pytest.importorskip("torch")
 p24 = pytest.importorskip("structured_sparse_gemm_prune24_amd")
-OK, NULL, SHAPE, ALIGN, DTYPE, UNSUP, WS = (p24.P24_OK, p24.P24_ERR_NULL, p24.P24_ERR_SHAPE, p24.P24_ERR_ALIGN,
-                                            p24.P24_ERR_DTYPE, p24.P24_ERR_UNSUPPORTED, p24.P24_ERR_WORKSPACE)
+OK, NULL, SHAPE, ALIGN, DTYPE, UNSUP = (p24.P24_OK, p24.P24_ERR_NULL, p24.P24_ERR_SHAPE, p24.P24_ERR_ALIGN,
+                                        p24.P24_ERR_DTYPE, p24.P24_ERR_UNSUPPORTED)
 P = 1 << 20
 F32, BF16, E4 = 0, 1, 2
 
@@ -91,17 +91,7 @@ def test_product_refusals(L, code, args):
     v = dict(data=P, ws=P, M=32, K=64, X=P, ldx=64, xs=P, N=4, Y=P, yd=BF16, ldy=32, b=None, act=0, r=None, ldr=0)
     v.update(args)
     assert L.spmm24_f8(v["data"], v["ws"], v["M"], v["K"], v["X"], v["ldx"], v["xs"], v["N"], v["Y"], v["yd"], v["ldy"],
-                       v["b"], v["act"], v["r"], v["ldr"], None, 0, None) == code
-
-
-def test_product_needs_its_workspace(L):
-    """Wherever the product asks for a workspace, a missing, short or misaligned one is refused."""
-    for M, K, N in ((32, 64, 1), (4096, 4096, 1), (4096, 4096, 200), (256, 8192, 100), (8192, 8192, 8192)):
-        need = L.spmm24_f8_workspace_bytes(M, K, N)
-        call = lambda ws, n: L.spmm24_f8(P, P, M, K, P, K, P, N, P, BF16, M, None, 0, None, 0, ws, n, None)  # noqa: E731
-        if need:
-            assert call(None, 0) == WS and call(P, need - 1) == WS and call(None, need) == WS
-            assert call(P + 8, need) == ALIGN
+                       v["b"], v["act"], v["r"], v["ldr"], None) == code
 
 
 class _Dev:
@@ -155,6 +145,14 @@ def test_binding_refusals():
     dc = p24.Compressed24F8(_Dev(c.data), _Dev(c.scale), 32, 64)
     with pytest.raises(ValueError, match="features"):
         p24.spmm24_f8(p24.Compressed24F8(dc.data, dc.scale, 32, 128), dq)
+    with pytest.raises(ValueError, match="compressed form"):
+        p24.spmm24_f8(p24.Compressed24F8(_Dev(c.data[:5120]), dc.scale, 32, 64), dq)
+    with pytest.raises(ValueError, match="compressed form"):
+        p24.decompress_f8(p24.Compressed24F8(_Dev(c.data.to(torch.int32)), dc.scale, 32, 64))
+    with pytest.raises(ValueError, match="weight's scale"):
+        p24.spmm24_f8(p24.Compressed24F8(dc.data, _Dev(torch.ones(31)), 32, 64), dq)
+    with pytest.raises(ValueError, match="the weight is on"):
+        p24.spmm24_f8(p24.Compressed24F8(_Dev(c.data, "cuda:1"), dc.scale, 32, 64), dq)
     with pytest.raises(ValueError, match="act"):
         p24.spmm24_f8(dc, dq, act="swish")
     with pytest.raises(ValueError, match="bias"):

@@ -402,3 +402,16 @@ def test_smfmac_f8_lane_map(seed):
     assert f(ta.data_ptr(), tb.data_ptr(), tw.data_ptr(), d.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert np.array_equal(d.cpu().numpy().astype(np.float64), smfmac64_model(a, b, words))
+
+
+def test_example(monkeypatch, capsys):
+    """The example runs and is as near the fp64 layer as two 8-bit roundings allow."""
+    need_gpu()
+    import os
+    import runpy
+    import sys
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward_f8.py")
+    monkeypatch.setattr(sys, "argv", [path, "--tokens", "5", "--width", "256", "--hidden", "448", "--steps", "2"])
+    runpy.run_path(path, run_name="__main__")
+    line = capsys.readouterr().out
+    assert "5 tokens, 256 -> 448 -> 256" in line and float(line.split("error")[1]) < 0.15
