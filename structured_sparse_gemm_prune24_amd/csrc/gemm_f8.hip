@@ -771,7 +771,7 @@ static F8Kernel choose_f8(const F8Args& a, bool exact) {
   }
   const int64_t tiles = f8_blocks(a, 32, 32);
   if (a.N <= 8 || (tiles <= 640 && a.K <= 1408)) return F8Kernel::TOKENS;
-  if (tiles <= 128 && !(exact && a.N > 32 && a.K >= 3072)) return F8Kernel::TOKENS;
+  if (tiles <= 128 && !(exact && a.N > 32 && a.K >= 2816)) return F8Kernel::TOKENS;
   const int64_t n128 = f8_blocks(a, 256, 128);
   // the widened operands of an fp32 output do not fit the registers of the two widest
   if (!exact) {
