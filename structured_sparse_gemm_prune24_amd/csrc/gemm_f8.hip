@@ -43,11 +43,33 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t v0, uint32_t v1) {
   return (bf16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// One lane's operands of a 64-k block of a 32 x 32 tile, and their product.  On
-// the bf16 unit instruction j takes stored values 8 j .. 8 j + 7 of each lane, which
-// are k 16 j + [0, 16) of lanes 0..31 and 32 + 16 j + [0, 16) of lanes 32..63; its
+// On the bf16 unit instruction j takes stored values 8 j .. 8 j + 7 of each lane,
+// which are k 16 j + [0, 16) of lanes 0..31 and 32 + 16 j + [0, 16) of lanes 32..63; its
 // token operand is then, in lane L, k 16 j + 8 (L / 32) + [0, 8) and the same 32
-// further on.
+// further on.  Of a 16 B chunk as the 8-bit unit takes it (k 16 (L / 32) + [0, 16))
+// that is its own half and the other lane's: one exchange between the halves of
+// the wave per register, after which register pair j belongs to instruction j.
+__device__ __forceinline__ u32x4 halves_by_instruction(u32x4 x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
+  return (u32x4){a[0], b[0], a[1], b[1]};
+}
+
+// The two bf16 products of a 64-k block: `lo` and `hi` are the token's two chunks
+// by instruction.
+__device__ __forceinline__ f32x16 exact_product(i32x4 w, int pos, u32x4 lo, u32x4 hi, f32x16 acc) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const bf16x16 b = __builtin_shufflevector(widen8(lo[2 * j], lo[2 * j + 1]), widen8(hi[2 * j], hi[2 * j + 1]), 0, 1, 2,
+                                              3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+    const bf16x8 a = widen8((uint32_t)w[2 * j], (uint32_t)w[2 * j + 1]);
+    acc = j == 0 ? __builtin_amdgcn_smfmac_f32_32x32x32_bf16(a, b, acc, pos, 0, 0)
+                 : __builtin_amdgcn_smfmac_f32_32x32x32_bf16(a, b, acc, pos, 0, 1);
+  }
+  return acc;
+}
+
+// One lane's operands of a 64-k block of a 32 x 32 tile, and their product.
 template <bool EXACT>
 struct F8Block {
   i32x4 a;
@@ -58,28 +80,11 @@ struct F8Block {
     a = *reinterpret_cast<const i32x4*>(w);
     pos = *reinterpret_cast<const int*>(p);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if constexpr (EXACT) {
-        const u32x2 lo = *reinterpret_cast<const u32x2*>(xp + 32 * q + 8 * half);
-        const u32x2 hi = *reinterpret_cast<const u32x2*>(xp + 32 * q + 16 + 8 * half);
-        x[q] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
-      } else {
-        x[q] = *reinterpret_cast<const u32x4*>(xp + 32 * q + 16 * half);
-      }
-    }
+    for (int q = 0; q < 2; ++q) x[q] = *reinterpret_cast<const u32x4*>(xp + 32 * q + 16 * half);
   }
   __device__ __forceinline__ f32x16 product(f32x16 acc) const {
     if constexpr (EXACT) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bf16x16 b = __builtin_shufflevector(widen8(x[0][2 * j], x[0][2 * j + 1]),
-                                                  widen8(x[1][2 * j], x[1][2 * j + 1]), 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10,
-                                                  11, 12, 13, 14, 15);
-        const bf16x8 av = widen8((uint32_t)a[2 * j], (uint32_t)a[2 * j + 1]);
-        acc = j == 0 ? __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, b, acc, pos, 0, 0)
-                     : __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, b, acc, pos, 0, 1);
-      }
-      return acc;
+      return exact_product(a, pos, halves_by_instruction(x[0]), halves_by_instruction(x[1]), acc);
     } else {
       const i32x8 b = __builtin_shufflevector(__builtin_bit_cast(i32x4, x[0]), __builtin_bit_cast(i32x4, x[1]), 0, 1, 2,
                                               3, 4, 5, 6, 7);
@@ -219,12 +224,6 @@ __device__ __forceinline__ i32x4 lds_b128(uint32_t addr) {
   return v;
 }
 template <int OFF>
-__device__ __forceinline__ u32x2 lds_b64(uint32_t addr) {
-  u32x2 v;
-  asm volatile("ds_read_b64 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
-  return v;
-}
-template <int OFF>
 __device__ __forceinline__ int lds_b32(uint32_t addr) {
   int v;
   asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
@@ -232,13 +231,12 @@ __device__ __forceinline__ int lds_b32(uint32_t addr) {
 }
 
 // The fragments of one 64-k block in a wave: weights, positions, tokens.
-template <int TM, int TN, bool EXACT>
+template <int TM, int TN>
 struct F8Frags {
-  static constexpr int PIECES = EXACT ? 4 : 2;             // LDS reads per token fragment
-  typedef typename std::conditional<EXACT, u32x2, i32x4>::type Piece;
+  static constexpr int PIECES = 2;                         // LDS reads per token fragment
   i32x4 a[TM];
   int pos[TM];
-  Piece b[TN][PIECES];
+  i32x4 b[TN][PIECES];
   // ties every register to the wait: no use moves above it
   __device__ __forceinline__ void tie() {
 #pragma unroll
@@ -274,7 +272,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   using C = F8Tile<BM, BN, WGM, WGN, LW, KG>;
   constexpr bool EXACT = sizeof(OutT) == 4, INPLACE = !EXACT && KG == 1;
   constexpr int TM = C::TM, TN = C::TN, NSTAGE = C::NSTAGE;
-  typedef F8Frags<TM, TN, EXACT> Frags;
+  typedef F8Frags<TM, TN> Frags;
   __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KG * NSTAGE * C::STAGE + (INPLACE ? C::SCALES : 0)];
 
   const int lane = threadIdx.x & 63, h = lane >> 5;
@@ -381,9 +379,9 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   for (int ss = 0; ss < 2; ++ss)
 #pragma unroll
     for (int q = 0; q < Frags::PIECES; ++q) {
-      // piece q: 16 B chunk 2 q + h of the block's four, or 8 B half h of chunk q
-      const int c = 4 * ss + (EXACT ? q : 2 * q + h);
-      b_addr[ss][q] = lds_base + b_row + (uint32_t)((c ^ (nl & 7)) * 16) + (EXACT ? 8 * h : 0);
+      // piece q: 16 B chunk 2 q + h of the block's four
+      const int c = 4 * ss + 2 * q + h;
+      b_addr[ss][q] = lds_base + b_row + (uint32_t)((c ^ (nl & 7)) * 16);
     }
   // row blocks wm * TM .. of the tile: group wm * TM / RBG (a wave's rows lie in one group, or are whole groups)
   const uint32_t a_group = lds_base + C::X_BYTES + (uint32_t)(wm * TM / C::RBG) * (C::UNITS * 1024);
@@ -404,8 +402,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
       f.a[i] = lds_b128<off>(a_addr + st);
     } else {
       constexpr int j = (r - 2 * TM) / Frags::PIECES, q = (r - 2 * TM) % Frags::PIECES;
-      if constexpr (EXACT) f.b[j][q] = lds_b64<j * 4096>(b_addr[ss][q] + st);
-      else f.b[j][q] = lds_b128<j * 4096>(b_addr[ss][q] + st);
+      f.b[j][q] = lds_b128<j * 4096>(b_addr[ss][q] + st);
     }
   };
 
@@ -424,15 +421,8 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     static_for<0, NM>([&](auto K) {
       constexpr int k = decltype(K)::value, i = k / TN, j = k % TN;
       if constexpr (EXACT) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const bf16x8 av = widen8((uint32_t)f.a[i][2 * u], (uint32_t)f.a[i][2 * u + 1]);
-          const bf16x16 bv =
-              __builtin_shufflevector(widen8(f.b[j][u][0], f.b[j][u][1]), widen8(f.b[j][2 + u][0], f.b[j][2 + u][1]), 0,
-                                      1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-          acc[i][j] = u == 0 ? __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, bv, acc[i][j], f.pos[i], 0, 0)
-                             : __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av, bv, acc[i][j], f.pos[i], 0, 1);
-        }
+        acc[i][j] = exact_product(f.a[i], f.pos[i], halves_by_instruction(__builtin_bit_cast(u32x4, f.b[j][0])),
+                                  halves_by_instruction(__builtin_bit_cast(u32x4, f.b[j][1])), acc[i][j]);
       } else {
         const i32x8 bv = __builtin_shufflevector(f.b[j][0], f.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
         acc[i][j] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(f.a[i], bv, acc[i][j], f.pos[i], 0, 0);
@@ -746,9 +736,7 @@ static p24_status launch_tile(F8Args a, hipStream_t st) {
 // 6.2; 1024 x 8192, one token 5.7, 8.5), at most 640 with a short K (4096 x 512, 128
 // tokens 3.8, 4.0; 1000 x 1024, 400 tokens 4.8, 5.0; but 8192 x 1024, 128 tokens 7.6,
 // 64x64 4.9), and with few tokens (16384 x 4096, one token 8.8, 64x64 9.6; but 24
-// tokens 11.5, 64x32 10.2).  With an fp32 output every 32 x 32 tile widens its
-// operands anew, and a long K makes that the larger part (140 x 5632, 684 tokens
-// 15.5, 64x32 11.1).
+// tokens 11.5, 64x32 10.2).
 // Over 260 shapes drawn at random the choice was 1.6 % behind the fastest of the
 // eight kernels (geometric mean).
 enum class F8Kernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x192, T256x256 };
@@ -770,8 +758,7 @@ static F8Kernel choose_f8(const F8Args& a, bool exact) {
     if (is("256x256")) return F8Kernel::T256x256;
   }
   const int64_t tiles = f8_blocks(a, 32, 32);
-  if (a.N <= 8 || (tiles <= 640 && a.K <= 1408)) return F8Kernel::TOKENS;
-  if (tiles <= 128 && !(exact && a.N > 32 && a.K >= 2816)) return F8Kernel::TOKENS;
+  if (a.N <= 8 || tiles <= 128 || (tiles <= 640 && a.K <= 1408)) return F8Kernel::TOKENS;
   const int64_t n128 = f8_blocks(a, 256, 128);
   // the widened operands of an fp32 output do not fit the registers of the two widest
   if (!exact) {
@@ -804,7 +791,7 @@ static p24_status launch_f8(const F8Args& a, hipStream_t st) {
     case F8Kernel::T64x64:
       if (long_k && f8_blocks(a, 64, 64) <= 256) {
         // widening is the larger part of an fp32 output's work: taller wave tiles
-        // widen each operand for more multiplies (1000 x 4032 with 517 tokens 13.2 -> 12.1)
+        // widen each operand for more multiplies (1000 x 4032 with 517 tokens 13.3 -> 11.9)
         if constexpr (EXACT) return launch_tile<64, 64, 1, 2, 2, 4, OutT>(a, st);
         else return launch_tile<64, 64, 2, 2, 4, 2, OutT>(a, st);
       }
