@@ -150,7 +150,7 @@ __global__ __launch_bounds__(W * 64) void k_f8_tokens(const F8Args args) {
     float z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] = fmaf(sum[i] * sx, ws[i], bs[i]);
-    f8_act(z, args.act);
+    f8_act<sizeof(OutT) == 4>(z, args.act);
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] += r[i];
     store_row<4>((OutT*)args.Y + (int64_t)n * args.ldy + m, args.M - m, z);
@@ -571,7 +571,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
             for (int u = 0; u < 4; ++u) z[4 * q + u] += b4[u];
           }
         }
-        f8_act(z, args.act);
+        f8_act<sizeof(OutT) == 4>(z, args.act);
         uint8_t* place[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -667,7 +667,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
 #pragma unroll
           for (int i = 0; i < 8; ++i) z[8 * t + i] = fmaf(i < 4 ? lo[i] : hi[i - 4], ws[i], bs[i]);
         }
-        f8_act(z, args.act);
+        f8_act<sizeof(OutT) == 4>(z, args.act);
         if (args.residual) {
           float r[U][8];
 #pragma unroll

@@ -108,7 +108,7 @@ __global__ __launch_bounds__(G ? 256 : 1024) void k_rows(const RowArgs args) {
   const __amdgpu_buffer_rsrc_t h_rsrc = f8_rsrc((const uint8_t*)((const T*)args.h + row * args.ldh), (uint32_t)width * sizeof(T));
   if constexpr (!NORM) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) f8_act(v[e], args.act);
+    for (int e = 0; e < E; ++e) f8_act<sizeof(OutT) == 4>(v[e], args.act);
   }
   if (b) {
 #pragma unroll

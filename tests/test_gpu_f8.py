@@ -86,7 +86,7 @@ def test_gate(tokens, width, pad, name, stream, out):
         got = p24.gated_act(gate, up, act=name, out_dtype=out)
         z = gate.to(D)
         e = act(z, name)
-        rel = act_error(z, name) + U
+        rel = act_error(z, name, out) + U
         if with_up:
             e = e * up.to(D)
         _check_rows(got, e, rel, out)
@@ -179,7 +179,7 @@ def _product_ref(c, x, bias, name, r, out):
         z = z + bias.to(D)
         err = err + 2 * U * z.abs()
     e = act(z, name)
-    err = 1.13 * err + act_error(z, name) * e.abs()      # no activation's slope passes 1.13
+    err = 1.13 * err + act_error(z, name, out) * e.abs()      # no activation's slope passes 1.13
     if r is not None:
         e = e + r.to(D)
         err = err + U * e.abs()
@@ -402,6 +402,33 @@ def test_smfmac_f8_lane_map(seed):
     assert f(ta.data_ptr(), tb.data_ptr(), tw.data_ptr(), d.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert np.array_equal(d.cpu().numpy().astype(np.float64), smfmac64_model(a, b, words))
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: their last rows are those of a call on the last rows alone."""
+    need_gpu()
+    tokens, width, last = 262200, 8256, 70
+    x = torch.empty(tokens, width, dtype=torch.bfloat16, device="cuda")
+    x[:-last] = 0
+    x[-last:] = _rows(3, last, width, 0, torch.bfloat16)
+    w = torch.rand(width, device="cuda")
+    y, h = p24.rms_norm(x, w, residual=x)
+    y1, h1 = p24.rms_norm(x[-last:], w, residual=x[-last:])
+    assert torch.equal(h[-last:], h1) and torch.equal(y.values[-last:].view(torch.uint8), y1.values.view(torch.uint8))
+    assert torch.equal(y.scale[-last:], y1.scale) and not h[:8].any()
+    del h, h1
+    a, a1 = p24.gated_act(x, x), p24.gated_act(x[-last:], x[-last:])
+    assert torch.equal(a.values[-last:].view(torch.uint8), a1.values.view(torch.uint8))
+    del a, x
+    # whole numbers: the sums are exact in whichever order the two calls take
+    q = torch.zeros(tokens, 128, device="cuda")
+    q[-last:] = torch.randint(-4, 5, (last, 128), device="cuda").float()
+    q = p24.Quantized8(q.to(F8), torch.ones(tokens, device="cuda"))
+    c = p24.compress_f8(torch.cat([torch.full((width, 64), 7.0, device="cuda"),
+                                   torch.randint(-6, 7, (width, 64), device="cuda").float()], 1))
+    Y = p24.spmm24_f8(c, q)
+    Y1 = p24.spmm24_f8(c, p24.Quantized8(q.values[-last:], q.scale[-last:]))
+    assert torch.equal(Y[-last:], Y1) and Y1.any() and not Y[:8].any()
 
 
 def test_example(monkeypatch, capsys):
