@@ -1,14 +1,26 @@
 // Compression of 8-bit 2:4 weights and its inverse.  Run once when a weight is
-// loaded: bound by the read of W (the second kernel finds most of it in the
-// Infinity Cache).
+// loaded: bound by its two reads of W (8192 x 8192 fp32 109 us, 5 TB/s; 188 with a
+// lane per operand lane, whose loads stride by rows).
 #include "p24_api_internal.hpp"
 #include "p24_f8.hpp"
 
 namespace p24 {
 
-template <typename T> __device__ __forceinline__ float w_value(T v);
-template <> __device__ __forceinline__ float w_value<float>(float v) { return v; }
-template <> __device__ __forceinline__ float w_value<uint16_t>(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+// Four consecutive weights, at any alignment.
+template <typename T>
+__device__ __forceinline__ void w_group(const T* w, float (&f)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    const u32x4 x = *reinterpret_cast<const u32x4_a4*>(w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(x[i]);
+  } else {
+    const u32x2 x = *reinterpret_cast<const u32x2_a2*>(w);
+    f[0] = bf16_lo(x[0]);
+    f[1] = bf16_hi(x[0]);
+    f[2] = bf16_lo(x[1]);
+    f[3] = bf16_hi(x[1]);
+  }
+}
 
 // One block per row: scale[m] = max(max|W[m][:]| / 448, 2^-126).  The row's
 // largest magnitude is always kept by the 2:4 selection, so the scale of the
@@ -17,7 +29,12 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_f8_scale(const T* W, int64_t ldw, int K, float* scale) {
   const T* w = W + (int64_t)blockIdx.x * ldw;
   uint32_t top = 0;
-  for (int k = threadIdx.x; k < K; k += 256) top = max(top, mag(w_value<T>(w[k])));
+  for (int k = 4 * threadIdx.x; k < K; k += 1024) {
+    float f[4];
+    w_group<T>(w + k, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, mag(f[i]));
+  }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     const uint32_t other = __shfl_xor(top, o);
@@ -30,9 +47,10 @@ __global__ __launch_bounds__(256) void k_f8_scale(const T* W, int64_t ldw, int K
     scale[blockIdx.x] = f8_scale(__uint_as_float(max(max(tops[0], tops[1]), max(tops[2], tops[3]))));
 }
 
-// One wave per (32-row block, 64-k block): lane L compresses row L % 32,
-// k 32 (L / 32) .. +32 of the block, eight groups of four, into its 16 values and
-// its position word.
+// One wave per (32-row block, 64-k block), four rows at a time: a lane compresses
+// one group of four, so that a row's 64 weights are one run of the load; eight
+// lanes then join their pairs of values and their positions into the 16 B and the
+// word of an operand lane.
 template <typename T>
 __global__ __launch_bounds__(256) void k_f8_compress(const T* W, int64_t ldw, int64_t M, int K, int64_t steps,
                                                      int64_t nblocks, const float* scale, uint8_t* data) {
@@ -40,30 +58,37 @@ __global__ __launch_bounds__(256) void k_f8_compress(const T* W, int64_t ldw, in
   const int64_t q = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // (row block, step)
   if (q >= nblocks) return;
   const int64_t rb = q / steps, s = q % steps;
-  const int64_t row = rb * 32 + (lane & 31);
-  const int64_t k0 = s * 64 + 32 * (lane >> 5);
-  uint32_t v[4] = {0, 0, 0, 0}, pos = 0x44444444u;
-  if (row < M && k0 < K) {    // K % 64 == 0: a half block is inside or outside
-    const T* w = W + row * ldw + k0;
-    const float sc = scale[row];
-    pos = 0;
+  const int g = lane % 16, j = g % 8;                               // group of the row, of the operand lane
+  const int64_t k = s * 64 + 4 * g;
+  uint8_t* piece = data + ((rb / 4) * steps + s) * F8_PIECE;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
+  for (int it = 0; it < 8; ++it) {
+    const int r = it * 4 + lane / 16;
+    const int64_t row = rb * 32 + r;
+    uint32_t two = 0, code = 0x4u;      // padding: zeros at positions 0, 1
+    if (row < M && k < K) {
       float f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = w_value<T>(w[4 * g + i]);
-      const uint32_t code = select_2of4(mag(f[0]), mag(f[1]), mag(f[2]), mag(f[3]));
+      w_group<T>(W + row * ldw + k, f);
+      const float sc = scale[row];
+      code = select_2of4(mag(f[0]), mag(f[1]), mag(f[2]), mag(f[3]));
       const uint32_t p0 = code & 3u, p1 = code >> 2;
       const float a = p0 == 0 ? f[0] : p0 == 1 ? f[1] : f[2];
       const float b = p1 == 1 ? f[1] : p1 == 2 ? f[2] : f[3];
-      const uint32_t two = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a / sc, b / sc, 0, false) & 0xFFFFu;
-      v[g / 2] |= two << (16 * (g & 1));
-      pos |= code << (4 * g);
+      two = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a / sc, b / sc, 0, false) & 0xFFFFu;
+    }
+    const uint32_t pair = two | (__shfl_xor(two, 1) << 16);         // whole in even lanes
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl(pair, (lane & ~7) + 2 * i);
+    uint32_t pos = code << (4 * j);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) pos |= __shfl_xor(pos, o);
+    if (j == 0) {
+      const int L = r + 32 * (g / 8);
+      *reinterpret_cast<u32x4*>(piece + (rb % 4) * 1024 + L * 16) = v;
+      *reinterpret_cast<uint32_t*>(piece + 4096 + (rb % 4) * 256 + L * 4) = pos;
     }
   }
-  uint8_t* piece = data + ((rb / 4) * steps + s) * F8_PIECE;
-  *reinterpret_cast<u32x4*>(piece + (rb % 4) * 1024 + lane * 16) = (u32x4){v[0], v[1], v[2], v[3]};
-  *reinterpret_cast<uint32_t*>(piece + 4096 + (rb % 4) * 256 + lane * 4) = pos;
 }
 
 __global__ __launch_bounds__(256) void k_f8_decompress(const uint8_t* data, const float* scale, int64_t M, int K,
