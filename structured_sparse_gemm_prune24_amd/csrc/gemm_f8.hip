@@ -162,51 +162,6 @@ __global__ __launch_bounds__(W * 64) void k_f8_tokens(const F8Args args) {
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void lds_void;
 
-// BM rows x BN tokens per block on WGM x WGN waves; K goes by 128 values (two
-// 64-k blocks) a step.  With KG > 1 there are KG such groups of waves, each with
-// its own stages and its own part of K.
-template <int BM, int BN, int WGM, int WGN, int LW_, int KG>
-struct F8Tile {
-  static constexpr int GWAVES = WGM * WGN;                 // waves of a group
-  static constexpr int WTM = BM / WGM, WTN = BN / WGN;     // wave tile
-  static constexpr int TM = WTM / 32, TN = WTN / 32;       // its 32 x 32 tiles
-  static constexpr int LW = LW_;                           // waves of a group that load
-  // stage: [X: BN rows of 128 B | per row group: two 64-k blocks of (row blocks' values, 1 KiB of positions)],
-  // with half a row group [.. | two row blocks' values of either 64-k block | 512 B of positions of each]
-  static constexpr int GROUPS = BM >= 128 ? BM / 128 : 1;
-  static constexpr int RBG = BM >= 128 ? 4 : BM / 32;      // row blocks used of a group
-  static constexpr int UNITS = RBG == 4 ? 10 : 2 * RBG + 1;   // 1 KiB loads of a group's step
-  static constexpr int BLOCK = RBG == 4 ? 5120 : RBG * 1024;  // from one 64-k block's values to the next's
-  static constexpr int P_FIRST = RBG == 4 ? 4096 : 2 * BLOCK, P_NEXT = RBG == 4 ? BLOCK : 512;   // the same of positions
-  static constexpr int X_BYTES = BN * 128, A_BYTES = GROUPS * UNITS * 1024;
-  static constexpr int STAGE = X_BYTES + A_BYTES;
-  static constexpr int NSTAGE = 3 * KG * STAGE <= 160 * 1024 ? 3 : 2;
-  static constexpr int X_DMA = BN / 8 / LW;                // 1 KiB loads per loading wave and step
-  static constexpr int A_LOADS = A_BYTES / 1024;
-  // A remainder of one load is left to one wave; of two, the other two waves repeat
-  // a load, which is cheaper than uneven counts (4096 x 2304 x 768 in 128 x 128: 13.9 us, 14.9).
-  static constexpr int A_DMA = (A_LOADS + LW - 1) / LW;
-  static constexpr int A_LAST = A_LOADS % LW == 1 ? 1 : 0;   // waves that issue the last one (0: all)
-  static constexpr int DMA = X_DMA + A_DMA;
-  static_assert(BM % (32 * WGM) == 0 && BN % (32 * WGN) == 0, "whole 32 x 32 tiles per wave");
-  static_assert((BN / 8) % LW == 0 && LW % 2 == 0 && LW <= GWAVES, "even X loads");
-  static_assert(BM % 128 == 0 || BM == 64, "whole row groups, or half of one");
-  static_assert(NSTAGE * KG * STAGE <= 160 * 1024, "LDS");
-  static_assert(NSTAGE * DMA < 64, "vmcnt range");
-  // epilogue by slices (fp32 outputs, split K): each wave turns one 32-token slice at a time through LDS
-  static constexpr int PITCH = WTM + 4;                    // floats per token
-  static_assert(GWAVES * 32 * PITCH * 4 <= NSTAGE * STAGE, "the slices fit the stages' LDS");
-  // epilogue in place (bf16 outputs): each wave's output tile as bf16, RPS of them in a stage
-  static constexpr int REGION = WTM * WTN * 2, RL = REGION / 1024;   // bytes, and 1 KiB loads of its residual
-  static constexpr int RPS = STAGE / REGION < GWAVES ? STAGE / REGION : GWAVES;
-  static constexpr int RDMA = RPS * RL / LW;               // residual loads per loading wave and stage
-  static constexpr int CH = WTM / 8;                       // 16 B chunks per token of a region
-  static constexpr int X_SCALES = BN < 64 ? 64 : BN;
-  static constexpr int SCALES = (2 * BM + X_SCALES) * 4;   // weight scales, bias, token scales
-  static_assert(RPS >= 1 && (RPS * RL) % LW == 0 && RDMA <= DMA, "residual loads take the place of a step's loads");
-  static_assert((GWAVES + RPS - 1) / RPS <= NSTAGE, "the regions fit the stages");
-};
-
 template <int I, int N, typename F>
 __device__ __forceinline__ void static_for(F&& f) {
   if constexpr (I < N) {
@@ -297,37 +252,18 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   const int k_first = (int)((int64_t)nk * kg / KG), count = (int)((int64_t)nk * (kg + 1) / KG) - k_first;
   const uint32_t lds_base = (uint32_t)(uintptr_t)(lds_void*)lds;
 
-  // X: load q of the tile brings 8 tokens x 128 B.  LDS slot of (token n, 16 B
-  // chunk c) = (n ^ ((n >> 3) & 1)) * 8 + (c ^ (n & 7)): sixteen consecutive tokens at
-  // one chunk fall on sixteen bank groups.  Tokens past N lie past the resource.
-  // In the last step of an odd count of 64-k blocks chunks 4..7 repeat chunks
-  // 0..3: they meet the weights' zero padding.
   const int n_rows = min(args.N - n0, BN);
   const __amdgpu_buffer_rsrc_t x_rsrc =
-      f8_rsrc(args.X + (int64_t)n0 * ldx, (uint32_t)((int64_t)(n_rows - 1) * ldx + args.K));
-  const int x_row = 8 * wave + ((lane >> 3) ^ (wave & 1));      // q = wave; the other loads keep its parity
-  const int x_chunk = (lane & 7) ^ (x_row & 7);
-  const uint32_t x_voff = (uint32_t)(x_row * ldx + 16 * x_chunk);
-  const uint32_t x_tail = x_voff - ((args.K & 64) && x_chunk >= 4 ? 64 : 0);
-  const uint32_t x_jump = (uint32_t)(8 * C::LW * ldx);
-  // weights: load q is unit q % UNITS of row group q / UNITS: the pieces of its two
-  // 64-k blocks in order, or of half a group two row blocks' values of each, then
-  // the positions, 512 B of either
-  const int g0 = m0 / 128;
-  const int g_count = min((int)f8_groups(args.M) - g0, C::GROUPS);
+      f8_rsrc(args.X + (int64_t)n0 * ldx, F8XReads<C>::bytes(n_rows, ldx, args.K));
+  const F8XReads<C> x_reads(lane, wave, ldx, args.K);
+  const F8WReads<C> w_reads(m0, args.M, args.K);
   const __amdgpu_buffer_rsrc_t a_rsrc =
-      f8_rsrc(args.W + (int64_t)g0 * steps * F8_PIECE, (uint32_t)g_count * steps * F8_PIECE);
-  const uint32_t a_voff = (uint32_t)lane * 16;
-  const uint32_t p_voff = (uint32_t)(lane / 32) * F8_PIECE + (uint32_t)(lane % 32) * 16;
-  const uint32_t first_rb = (uint32_t)(m0 / 32) % 4;        // half a group: its first row block
+      f8_rsrc(args.W + (int64_t)(m0 / 128) * steps * F8_PIECE, w_reads.bytes());
   uint32_t a_soff[C::A_DMA], a_dst[C::A_DMA];
 #pragma unroll
   for (int j = 0; j < C::A_DMA; ++j) {
-    const int q = min(j * LW + wave, C::A_LOADS - 1), u = q % C::UNITS;
-    a_dst[j] = C::X_BYTES + q * 1024;
-    const uint32_t grp = (uint32_t)(q / C::UNITS) * steps * F8_PIECE;
-    if constexpr (C::RBG == 4) a_soff[j] = grp + u * 1024;
-    else a_soff[j] = u == 2 * C::RBG ? 4096 + first_rb * 256 : (u / C::RBG) * F8_PIECE + (first_rb + u % C::RBG) * 1024;
+    a_dst[j] = C::X_BYTES + w_reads.unit(j, wave) * 1024;
+    a_soff[j] = w_reads.scalar(j, wave);
   }
   const bool last_load = C::A_LAST == 0 || wave < C::A_LAST;
   const bool loader = wave < C::LW;
@@ -338,34 +274,33 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     uint8_t* stage = lds + st;
     const int g = k_first + min(it, count - 1);
     if constexpr (q < C::X_DMA) {
-      const uint32_t voff = g == nk - 1 ? x_tail : x_voff;
-      load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, voff, (uint32_t)g * 128 + q * x_jump);
+      uint32_t rows = x_reads.rows(q);
+      asm volatile("" : "+s"(rows));   // added here: kept over the loop, the loads' offsets would take a register each
+      load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, x_reads.vector(rows, g == nk - 1), x_reads.scalar(g));
     } else {
       constexpr int j = q - C::X_DMA;
       if (C::A_LAST != 0 && j == C::A_DMA - 1 && !last_load) return;
-      const uint32_t voff = C::RBG < 4 && (j * LW + wave) % C::UNITS == 2 * C::RBG ? p_voff : a_voff;
-      load_to_lds(a_rsrc, stage + a_dst[j], voff, (uint32_t)g * (2 * F8_PIECE) + a_soff[j]);
+      load_to_lds(a_rsrc, stage + a_dst[j], w_reads.vector(lane, j, wave), (uint32_t)g * (2 * F8_PIECE) + a_soff[j]);
     }
   };
 
   // The residual of region r (wave r's output tile) on its way to LDS, in the
   // stages that the last steps leave free: RPS regions a stage, the stage of
-  // "step" count + r / RPS.  A region is [token][16 B chunk c of its features] with
-  // chunk c of token t at place c ^ (t % CH): both the accumulators' order (one
-  // feature quad of 32 tokens) and whole rows then spread over the banks.
+  // "step" count + r / RPS.  A region is [token][16 B chunk c of its features], the
+  // chunks exchanged (f8_residual_vector) so that both the accumulators' order (one
+  // feature quad of 32 tokens) and whole rows spread over the banks.
   const __amdgpu_buffer_rsrc_t r_rsrc =
       f8_rsrc((const uint8_t*)args.residual + ((int64_t)n0 * args.ldr + m0) * 2,
-              (uint32_t)(INPLACE && args.res_dma ? ((int64_t)(n_rows - 1) * args.ldr + args.M - m0) * 2 : 0));
+              INPLACE && args.res_dma ? f8_residual_bytes<C>(n_rows, args.ldr, args.M - m0) : 0u);
   const int r_t = lane / C::CH;                                  // token of a lane in its load, 64 / CH a load
   auto issue_residual = [&](auto Q, int it, uint32_t st) {
     constexpr int q = decltype(Q)::value;
     const int l = q * LW + wave;                                 // load l of the stage, of its region l / RL
     const int r = (it - count) * C::RPS + l / C::RL;
     if (q < C::RDMA && r < C::GWAVES) {
-      const int t = (l % C::RL) * (64 / C::CH) + r_t;            // token of the region
-      const int chunk = (lane % C::CH) ^ (t % C::CH);
-      load_to_lds(r_rsrc, lds + st + l * 1024, (uint32_t)((t * args.ldr + 8 * chunk) * 2),
-                  (uint32_t)(((r % WGN) * C::WTN * args.ldr + (r / WGN) * C::WTM) * 2));
+      int ln = lane;
+      asm volatile("" : "+v"(ln));   // the offsets of each load, too, are not kept over the loop
+      load_to_lds(r_rsrc, lds + st + l * 1024, f8_residual_vector<C>(ln, l, r, WGN, (uint32_t)args.ldr * 2), 0);
     } else if (it == count || it < NSTAGE) {
       issue(Q, it, st);     // until the last step has landed the waits count on a whole step's loads
     }
@@ -456,10 +391,10 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     const __amdgpu_buffer_rsrc_t bs =
         f8_rsrc((const uint8_t*)(args.bias ? args.bias + m0 : nullptr), args.bias ? (uint32_t)(args.M - m0) * 4 : 0);
     const __amdgpu_buffer_rsrc_t xs = f8_rsrc((const uint8_t*)(args.x_scale + n0), (uint32_t)n_rows * 4);
-    for (int u = wave; u < BM / 64; u += C::GWAVES) load4_to_lds(ws, sc + u * 256, lane * 4, u * 256);
+    for (int u = wave; u < BM / 64; u += C::GWAVES) load4_to_lds(ws, sc + u * 256, lane * 4 + u * 256, 0);
     if (args.bias)
-      for (int u = wave; u < BM / 64; u += C::GWAVES) load4_to_lds(bs, sc + BM * 4 + u * 256, lane * 4, u * 256);
-    for (int u = wave; u < C::X_SCALES / 64; u += C::GWAVES) load4_to_lds(xs, sc + BM * 8 + u * 256, lane * 4, u * 256);
+      for (int u = wave; u < BM / 64; u += C::GWAVES) load4_to_lds(bs, sc + BM * 4 + u * 256, lane * 4 + u * 256, 0);
+    for (int u = wave; u < C::X_SCALES / 64; u += C::GWAVES) load4_to_lds(xs, sc + BM * 8 + u * 256, lane * 4 + u * 256, 0);
   }
 #pragma unroll
   for (int g = 0; g < NSTAGE; ++g)

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "p24_device.hpp"
+#include "p24_f8_tile.hpp"
 #include "../../include/prune24_f8.h"
 
 namespace p24 {
@@ -11,11 +12,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr float F8_MAX = 448.0f;
 constexpr float F32_TINY = 1.17549435e-38f;   // 2^-126
-
-// The layout of compressed 8-bit weights (include/prune24_f8.h).
-constexpr int F8_PIECE = 5120;                // one row group's 64-k block: 4 x 1 KiB values, 4 x 256 B positions
-__host__ __device__ inline int64_t f8_groups(int64_t M) { return (M + 127) / 128; }
-__host__ __device__ inline int64_t f8_steps(int64_t K) { return 2 * ((K + 127) / 128); }
 
 // Vectors loaded and stored at any element alignment: rows of an odd leading
 // dimension start anywhere, and global memory takes such accesses whole.
