@@ -43,6 +43,7 @@
 
 #include "p24_api_internal.hpp"
 #include "p24_device.hpp"
+#include "p24_reads.hpp"
 
 namespace p24 {
 
@@ -325,25 +326,16 @@ __global__ __launch_bounds__(WGM * WGN * 64) void k_gemm(const GemmArgs args) {
   // rows over the 8 slots of a half, so 16 consecutive n at one chunk (one
   // quarter of a 16-byte-per-lane read) hit 16 distinct bank groups.  Load j of
   // this wave fills slots [(j*NWAVES + wave)*64, +64): rows 8q .. 8q+7, q = j*NWAVES + wave.
-  uint32_t xt_jstride = 0;
   if constexpr (XT) {
-    const int q = wave;                                     // j = 0
-    const int n_loc = 8 * q + ((lane >> 3) ^ (q & 1));      // row' = 8q + lane/8, n = row' ^ (q & 1)
-    const int c = (lane & 7) ^ (n_loc & 7);
-    x_voff = (uint32_t)(n_loc * ldx + 8 * c) * 2;
-    xt_jstride = (uint32_t)(8 * C::LW * ldx * 2);           // q advances by LW (even: parity kept)
+    x_voff = xt_vector(lane, wave, ldx);                    // j = 0
     static_assert(C::LW % 2 == 0, "X^T loads keep the row-pair parity per wave");
   }
   // A values: load j fills the (row block, step) block q = j*NWAVES + wave of
   // the stage.  Metadata: wave w < MG loads group w (four row blocks, 1 KiB per
   // K-pair).  Only the lane part of an address is per lane; the block part is
-  // wave-uniform and goes into the scalar offset.  Blocks past the matrix read
-  // past the resource end and come back as zeros.
+  // wave-uniform and goes into the scalar offset.  Row blocks and groups past the
+  // matrix repeat its last one (their results are not stored).
   const uint32_t a_voff = (uint32_t)lane * 16;
-  auto a_block_off = [&](int j) -> uint32_t {
-    const int q = j * C::LW + wave;
-    return (uint32_t)(((q / ASTEPS) * S + q % ASTEPS) * 1024);
-  };
   const bool meta_wave = wave < C::MG;
   // waves with one load per step beyond their share of X and A: the metadata
   // loaders and, for a gather on the sparse MFMA, the wave that brings the
@@ -357,6 +349,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void k_gemm(const GemmArgs args) {
   const int g_end = ngroups < g0 + C::MG ? ngroups : g0 + C::MG;
   const __amdgpu_buffer_rsrc_t m_rsrc =
       SPARSE ? make_rsrc(Ameta + (int64_t)g0 * T_ * 256, (uint32_t)((g_end - g0) * T_ * 1024)) : a_rsrc;
+  auto a_block_off = [&](int j) { return a_scalar(j * C::LW + wave, ASTEPS, S, rb_end - rb0); };
   const int m_in_group = C::RB % 4 ? (rb0 & 3) : 0;        // first row block's place in its metadata group
   const int n_rows = N - n0 < BN ? N - n0 : BN;
   const __amdgpu_buffer_rsrc_t xt_rsrc =
@@ -428,7 +421,9 @@ __global__ __launch_bounds__(WGM * WGN * 64) void k_gemm(const GemmArgs args) {
         k = k < 0 ? 0 : (k >= args.Kx ? args.Kx - 1 : k);
         dma16_to_lds(xg_rsrc, stage + (j * C::LW + wave) * 1024, (uint32_t)(k * ldx * 2) + x_voff, 0);
       } else if constexpr (XT) {
-        dma16_to_lds(xt_rsrc, stage + (j * C::LW + wave) * 1024, x_voff, (uint32_t)g * BK * 2 + j * xt_jstride);
+        uint32_t rows = xt_rows(j * C::LW, ldx);
+        asm volatile("" : "+s"(rows));   // added here: kept over the loop, the loads' offsets would take a register each
+        dma16_to_lds(xt_rsrc, stage + (j * C::LW + wave) * 1024, x_voff + rows, (uint32_t)g * BK * 2);
       } else {
         const __amdgpu_buffer_rsrc_t xr = make_rsrc(args.X + (int64_t)g * BK * ldx, (uint32_t)(BK * ldx * 2));
         dma16_to_lds(xr, stage + (j * C::LW + wave) * 1024, x_voff, (uint32_t)(j * X_ROW_STEP * ldx * 2));
@@ -440,7 +435,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void k_gemm(const GemmArgs args) {
     } else if constexpr (SPARSE) {
       if (meta_wave)
         dma16_to_lds(m_rsrc, stage + C::X_BYTES + C::A_BYTES + wave * 1024, a_voff,
-                     (uint32_t)g * 1024 + (uint32_t)wave * T_ * 1024);
+                     (uint32_t)g * 1024 + meta_scalar(wave, T_, g_end - g0));
       else if (kept_wave)
         dma4_to_lds(k_rsrc, stage + K_OFF, k_voff, (uint32_t)min(g + NSTAGE, nk - 1) * BK * 4);
     }

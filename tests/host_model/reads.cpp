@@ -53,6 +53,33 @@ long f8_tile(int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldr) {
 
 }  // namespace
 
+// The bf16 products' loads for any tile: BM rows, BN columns, LW loading waves, whole row groups or a
+// part of one, sparse (asteps 2) or dense (4).
+extern "C" long bf16_bad_reads(int BM, int BN, int LW, int asteps, int64_t M, int64_t N, int64_t K, int64_t ldx) {
+  const int64_t S = asteps == 2 ? K / 32 : K / 16, T = K / 64;
+  const int RB = BM / 32, MG = RB % 4 ? RB / 4 + 1 : RB / 4;
+  const int nrb = (int)((M + 31) / 32), ngroups = (int)((M + 127) / 128);
+  long n_bad = 0;
+  for (int64_t m0 = 0; m0 < M; m0 += BM) {
+    const int rb0 = (int)(m0 / 32), rbs = std::min(nrb - rb0, RB), groups = std::min(ngroups - rb0 / 4, MG);
+    for (int lane = 0; lane < 64; ++lane)
+      for (int64_t g = 0; g < K / 64; ++g) {
+        for (int q = 0; q < RB * asteps; ++q)
+          n_bad += bad(lane * 16, g * asteps * 1024 + a_scalar(q, asteps, S, rbs), 16, rbs * S * 1024, (nrb - rb0) * S * 1024);
+        for (int w = 0; asteps == 2 && w < MG; ++w)
+          n_bad += bad(lane * 16, g * 1024 + meta_scalar(w, T, groups), 16, groups * T * 1024, (ngroups - rb0 / 4) * T * 1024);
+      }
+  }
+  for (int64_t n0 = 0; n0 < N; n0 += BN) {
+    const int64_t rows = std::min<int64_t>(N - n0, BN), end = (N - n0) * ldx * 2;
+    for (int lane = 0; lane < 64; ++lane)
+      for (int64_t g = 0; g < K / 64; ++g)
+        for (int q = 0; q < BN / 8; ++q)
+          n_bad += bad(xt_vector(lane, q % LW, ldx) + xt_rows(q / LW * LW, ldx), g * 128, 16, rows * ldx * 2, end);
+  }
+  return n_bad;
+}
+
 // The block tiles that spmm24_f8 launches, by place in its order.
 extern "C" long f8_bad_reads(int tile, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldr) {
   switch (tile) {
