@@ -1,12 +1,12 @@
 // Row operators around the 8-bit products: RMS norm with the residual's
 // addition, and the gated activation, each with an 8-bit, bf16 or fp32 output.
 //
-// One row (token) belongs to G threads, E chunks of 16 input bytes each,
+// One row (token) belongs to G threads, E <= 4 chunks of 16 input bytes each,
 // held in registers from the one read to the one write: the row's statistics
 // (sum of squares, largest magnitude) need the whole row before the first
 // output, and a second read would cost what the first did.  Bound by HBM: the
 // norm moves 7 bytes per value (bf16 in, residual, sum, 8-bit out), the gated
-// activation 5.
+// activation 5.  Rows past the registers are read twice (k_rows_wide).
 //
 // Norm: with r = 1 / sqrt(mean(h^2) + eps), y_i = h_i r w_i, so
 // max|y| = r max|h_i w_i|: the sum of squares and the maximum of |h w| come out
@@ -172,6 +172,90 @@ __global__ __launch_bounds__(G ? 256 : 1024) void k_rows(const RowArgs args) {
   }
 }
 
+// Rows past the registers of a block (more than 4 chunks of each of 1024 threads):
+// the statistics in one pass over the row, the outputs in a second one, whose
+// reads the caches serve in part.  A thread takes chunks t, t + threads, ..., U of
+// them on the way at a time; its values of a row are 64 at most.  `h` may be x or
+// the residual: it is written in the second pass, each chunk by the thread that has
+// read it.  Nothing spills, where 8 and 17 chunks held by a thread did, us:
+//   norm 4096 x 53248 bf16, 8-bit out   430 (3.6 TB/s of 7 B a value), held 882;  bf16 out 431, 1120
+//   norm 512 x 65535 bf16, 8-bit out     63, held 466;  512 x 53248 fp32 86, 198
+//   gate 4096 x 53248 bf16, 8-bit out   277 (3.9 TB/s of 5 B a value), held 511
+template <typename T, typename OutT, bool NORM>
+__global__ __launch_bounds__(1024) void k_rows_wide(const RowArgs args) {
+  constexpr int V = 16 / sizeof(T), U = sizeof(T) == 2 ? 2 : 4;
+  const int t = threadIdx.x, threads = args.threads, width = args.width;
+  const int64_t row = blockIdx.x;
+  const T* a = (const T*)args.a + row * args.lda;
+  const T* b = args.b ? (const T*)args.b + row * args.ldb : nullptr;
+  int d = 0;
+  if constexpr (sizeof(T) == 2)
+    if (args.shift) d = (int)((args.ref + row * args.ldref) % V);
+  const int chunks = (width + d + V - 1) / V;
+
+  // f(first value of the chunk, its values before the row's factors, the norm's weights)
+  auto each = [&](bool weights, auto&& f) {
+    for (int q0 = t; q0 < chunks; q0 += U * threads) {
+      float v[U][V], u[U][V], w[NORM ? U : 1][V];
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        const int c = (q0 + e * threads) * V - d;
+        load_row<V>(a + c, width - c, v[e], -c);
+        if (b) load_row<V>(b + c, width - c, u[e], -c);
+      }
+      if constexpr (NORM)
+        if (weights) {
+#pragma unroll
+          for (int e = 0; e < U; ++e) {
+            const int c = (q0 + e * threads) * V - d;
+            load_row<V>(args.weight + c, width - c, w[e], -c);
+          }
+        }
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        if constexpr (!NORM) f8_act<sizeof(OutT) == 4>(v[e], args.act);
+        if (b) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[e][i] = NORM ? v[e][i] + u[e][i] : v[e][i] * u[e][i];
+        }
+        f((q0 + e * threads) * V - d, v[e], w[NORM ? e : 0]);
+      }
+    }
+  };
+
+  float k = 1.0f, inv = 1.0f;
+  if constexpr (NORM || sizeof(OutT) == 1) {
+    float sum = 0.0f;
+    uint32_t top = 0;
+    each(sizeof(OutT) == 1, [&](int, float (&v)[V], float (&w)[V]) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (NORM) sum = fmaf(v[i], v[i], sum);
+        if constexpr (sizeof(OutT) == 1) top = max(top, mag(NORM ? v[i] * w[i] : v[i]));
+      }
+    });
+    row_reduce<0>(sum, top, threads);
+    if constexpr (NORM) k = 1.0f / sqrtf(sum / (float)width + args.eps);
+    if constexpr (sizeof(OutT) == 1) {
+      const float s = f8_scale(__uint_as_float(top) * k);
+      if (t == 0) args.scale[row] = s;
+      inv = 1.0f / s;
+    }
+  }
+  OutT* y = (OutT*)args.y + row * args.ldy;
+  T* h = NORM && b ? (T*)args.h + row * args.ldh : nullptr;
+  each(true, [&](int c, float (&v)[V], float (&w)[V]) {
+    if constexpr (NORM)
+      if (h) store_row<V>(h + c, width - c, v, -c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (NORM) v[i] = v[i] * w[i] * k;
+      if constexpr (sizeof(OutT) == 1) v[i] *= inv;
+    }
+    store_row<V>(y + c, width - c, v, -c);
+  });
+}
+
 template <typename T, typename OutT, int G, int E, bool NORM>
 static p24_status launch_rows(RowArgs a, int chunks, hipStream_t st) {
   const int per = G ? 256 / (G ? G : 1) : 1;                                       // rows of a block
@@ -214,8 +298,9 @@ static p24_status rows_by_width(RowArgs a, hipStream_t st) {
   if (chunks <= 640 || (sizeof(T) == 4 && chunks <= 1024)) return launch_rows<T, OutT, 0, 1, NORM>(a, chunks, st);
   if (chunks <= 2048) return launch_rows<T, OutT, 0, 2, NORM>(a, chunks, st);
   if (chunks <= 4096) return launch_rows<T, OutT, 0, 4, NORM>(a, chunks, st);
-  if (chunks <= 8192) return launch_rows<T, OutT, 0, 8, NORM>(a, chunks, st);
-  return launch_rows<T, OutT, 0, 17, NORM>(a, chunks, st);
+  a.threads = 1024;   // 4096 chunks and more
+  hipLaunchKernelGGL((k_rows_wide<T, OutT, NORM>), dim3((unsigned)a.rows), dim3(a.threads), 0, st, a);
+  return launch_status();
 }
 
 template <bool NORM>

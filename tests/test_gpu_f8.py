@@ -442,3 +442,37 @@ def test_example(monkeypatch, capsys):
     runpy.run_path(path, run_name="__main__")
     line = capsys.readouterr().out
     assert "5 tokens, 256 -> 448 -> 256" in line and float(line.split("error")[1]) < 0.15
+
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32], ids=["xbf16", "xf32"])
+@pytest.mark.parametrize("width,pad", [(32768, 0), (32769, 3), (53248, 0), (65529, 8), (65536, 0), (65536, 1)])
+def test_norm_adds_few_squares_in_turn(width, pad, stream):
+    """One value of 1 and the rest 2^-12: their squares are half an fp32 step of 1, so a thread that holds the 1
+    loses every square it adds in turn.  At most 64 squares a thread, and 22 steps after: 43 U after the root, and
+    8 U beside the sum."""
+    need_gpu()
+    x = torch.full((2, width + pad), 2.0 ** -12, dtype=stream, device="cuda")[:, :width]
+    x[:, 0] = 1
+    y, _ = p24.rms_norm(x, torch.ones(width, device="cuda"), out_dtype=torch.float32)
+    e = x.to(D) / torch.sqrt(x.to(D).square().mean(dim=1, keepdim=True) + 1e-6)
+    assert ((y.to(D) - e).abs() / e).max() <= 51 * U
+
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32], ids=["xbf16", "xf32"])
+@pytest.mark.parametrize("width,pad", [(16385, 0), (40001, 3), (53248, 0), (65536, 1)])
+def test_wide_norm_in_place(width, pad, stream):
+    """Rows that are read twice, with h in the place of x or of the residual."""
+    need_gpu()
+    x, r = _rows(6, 3, width, pad, stream), _rows(7, 3, width, 0, stream)
+    w = torch.rand(width, device="cuda")
+    for out in (F8, torch.float32):
+        y0, h0 = p24.rms_norm(x, w, residual=r, out_dtype=out)
+        assert torch.equal(h0, x + r)
+        for alias in ("x", "r"):
+            a, b = x.clone(), r.clone()
+            y, h = p24.rms_norm(a, w, residual=b, h=a if alias == "x" else b, out_dtype=out)
+            assert torch.equal(h, h0)
+            if out == F8:
+                assert torch.equal(y.values.view(torch.uint8), y0.values.view(torch.uint8))
+            else:
+                assert torch.equal(y, y0)
