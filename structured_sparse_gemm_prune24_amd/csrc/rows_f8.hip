@@ -10,7 +10,9 @@
 //
 // Norm: with r = 1 / sqrt(mean(h^2) + eps), y_i = h_i r w_i, so
 // max|y| = r max|h_i w_i|: the sum of squares and the maximum of |h w| come out
-// of one pass and one reduction.
+// of one pass and one reduction.  Where the squares leave fp32 (below, above
+// about 1e19), both are taken again from h f, f a power of two:
+// y = h f w / sqrt(mean (h f)^2 + eps f^2).
 #include "p24_api_internal.hpp"
 #include "p24_f8.hpp"
 
@@ -69,6 +71,14 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int thread
       top = max(top, i < waves ? m[i] : 0u);
     }
   }
+}
+
+// Factor of a norm's row (or of a thread's part of it) by its sum of squares.  Large
+// values overflow it, small ones lose bits that only an eps of 2^-100 or more covers.
+// (A NaN takes the factor of large values and stays.)
+__device__ __forceinline__ float norm_factor(float sum, float eps) {
+  if (sum < 0x1p-80f && eps < 0x1p-100f) return 0x1p100f;
+  return sum <= 0x1p120f ? 1.0f : 0x1p-80f;
 }
 
 // G lanes a row, several rows to a block of 256 threads; G = 0: a block a row.
@@ -134,25 +144,62 @@ __global__ __launch_bounds__(G ? 256 : 1024) void k_rows(const RowArgs args) {
   // values past the row are zero: act(0) = 0 for every activation
   float sum = 0.0f;
   uint32_t top = 0;
+  float part = 0.0f, ft = 1.0f;   // this thread's squares, of h ft, with a factor of its own; v becomes h ft w
+  if constexpr (NORM) {
+    auto squares = [&]() {
+      float p = 0.0f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (NORM) {
+      for (int e = 0; e < E; ++e)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        sum = fmaf(v[e][i], v[e][i], sum);
-        v[e][i] *= w[e][i];
-      }
+        for (int i = 0; i < V; ++i) p = fmaf(v[e][i], v[e][i], p);
+      return p;
+    };
+    part = sum = squares();
+    ft = norm_factor(sum, args.eps);
+    if (__builtin_expect(ft != 1.0f, 0)) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[e][i] *= ft;
+      part = squares();
     }
-    if constexpr (sizeof(OutT) == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[e][i] *= w[e][i];
+  }
+  if constexpr (sizeof(OutT) == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
 #pragma unroll
       for (int i = 0; i < V; ++i) top = max(top, mag(v[e][i]));
-    }
   }
   // two factors, not their product: with a tiny scale the product overflows
   float k = 1.0f, inv = 1.0f;
   if constexpr (NORM || sizeof(OutT) == 1) {
+    const float own = __uint_as_float(top);
+    if constexpr (NORM)
+      if (__builtin_expect(ft != 1.0f, 0)) top = mag(own * (1.0f / ft));
     row_reduce<G>(sum, top, threads);
-    if constexpr (NORM) k = 1.0f / sqrtf(sum / (float)width + args.eps);
+    if constexpr (NORM) {
+      // The row's factor.  A thread of large values makes it theirs, and a row of small
+      // ones has only such threads: where it is not this thread's, that is 1 or 2^100,
+      // and undone first nothing leaves fp32 that the row's result would show.
+      const float f = norm_factor(sum, args.eps), undo = 1.0f / ft;
+      if (__builtin_expect(f != 1.0f, 0)) {        // the whole row
+        sum = f == ft ? part : part * undo * undo * f * f;
+        top = f == ft ? mag(own) : mag(own * undo * f);
+        if constexpr (G == 0) __syncthreads();     // the first reduction's parts have been read
+        row_reduce<G>(sum, top, threads);
+      }
+      if (__builtin_expect(f != ft, 0)) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[e][i] = v[e][i] * undo * f;
+      }
+      k = 1.0f / sqrtf(sum / (float)width + args.eps * f * f);
+    }
     if constexpr (sizeof(OutT) == 1) {
       const float s = f8_scale(__uint_as_float(top) * k);
       if (t == 0) args.scale[row] = s;
@@ -223,19 +270,32 @@ __global__ __launch_bounds__(1024) void k_rows_wide(const RowArgs args) {
     }
   };
 
-  float k = 1.0f, inv = 1.0f;
+  float k = 1.0f, inv = 1.0f, f = 1.0f;
   if constexpr (NORM || sizeof(OutT) == 1) {
-    float sum = 0.0f;
-    uint32_t top = 0;
-    each(sizeof(OutT) == 1, [&](int, float (&v)[V], float (&w)[V]) {
+    float sum;
+    uint32_t top;
+    auto statistics = [&]() {
+      sum = 0.0f;
+      top = 0;
+      each(sizeof(OutT) == 1, [&](int, float (&v)[V], float (&w)[V]) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (NORM) sum = fmaf(v[i], v[i], sum);
-        if constexpr (sizeof(OutT) == 1) top = max(top, mag(NORM ? v[i] * w[i] : v[i]));
+        for (int i = 0; i < V; ++i) {
+          if constexpr (NORM) v[i] *= f;
+          if constexpr (NORM) sum = fmaf(v[i], v[i], sum);
+          if constexpr (sizeof(OutT) == 1) top = max(top, mag(NORM ? v[i] * w[i] : v[i]));
+        }
+      });
+      row_reduce<0>(sum, top, threads);
+    };
+    statistics();
+    if constexpr (NORM) {
+      f = norm_factor(sum, args.eps);
+      if (__builtin_expect(f != 1.0f, 0)) {
+        __syncthreads();
+        statistics();
       }
-    });
-    row_reduce<0>(sum, top, threads);
-    if constexpr (NORM) k = 1.0f / sqrtf(sum / (float)width + args.eps);
+      k = 1.0f / sqrtf(sum / (float)width + args.eps * f * f);
+    }
     if constexpr (sizeof(OutT) == 1) {
       const float s = f8_scale(__uint_as_float(top) * k);
       if (t == 0) args.scale[row] = s;
@@ -249,7 +309,7 @@ __global__ __launch_bounds__(1024) void k_rows_wide(const RowArgs args) {
       if (h) store_row<V>(h + c, width - c, v, -c);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if constexpr (NORM) v[i] = v[i] * w[i] * k;
+      if constexpr (NORM) v[i] = v[i] * f * w[i] * k;
       if constexpr (sizeof(OutT) == 1) v[i] *= inv;
     }
     store_row<V>(y + c, width - c, v, -c);

@@ -476,3 +476,71 @@ def test_wide_norm_in_place(width, pad, stream):
                 assert torch.equal(y.values.view(torch.uint8), y0.values.view(torch.uint8))
             else:
                 assert torch.equal(y, y0)
+
+
+@pytest.mark.parametrize("out", [F8, torch.bfloat16, torch.float32], ids=["f8", "bf16", "f32"])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32], ids=["xbf16", "xf32"])
+@pytest.mark.parametrize("width", [7, 100, 250, 700, 2049, 4097, 9000, 20001, 40001])
+def test_norm_of_rows_out_of_the_squares_range(width, stream, out):
+    """Rows whose squares leave fp32, up to the type's largest and down to its smallest values, with an eps under
+    and over them: the norm is the formula's, and the ordinary rows beside them keep their bits."""
+    need_gpu()
+    powers = [-130, -100, -63, -52, -45, -40, 50, 57, 60, 64, 90, 119]
+    base = _rows(61, 2 * len(powers) + 3, width, 0, torch.float32)
+    base = base.clamp(-60, 60)                               # below 2^6: the largest is 2^125
+    base[:len(powers)] = torch.stack([base[i] * 2.0 ** p for i, p in enumerate(powers)])
+    base[len(powers):2 * len(powers), width // 3] = torch.tensor([2.0 ** p for p in powers], device="cuda")   # one value
+    base[2 * len(powers), 0] = torch.finfo(stream).min
+    x = base.to(stream)
+    w = 1 + 0.1 * _rows(9, 1, width, 0, torch.float32)[0]
+    zero, clean = torch.zeros_like(x), x.clone()
+    clean[:-2] = 1                                           # the ordinary rows in the same places (order of their sums)
+    for eps in (0.0, 2.0 ** -120, 1e-6):
+        ordinary, _ = p24.rms_norm(clean, w, eps=eps, out_dtype=out)
+        for r in (None, zero):
+            y, h = p24.rms_norm(x, w, residual=r, eps=eps, out_dtype=out)
+            e = x.to(D)
+            e = e / torch.sqrt(e.square().mean(dim=1, keepdim=True) + eps) * w.to(D)
+            _check_rows(y, e, 64 * U, out)
+            assert h is None or torch.equal(h, x)
+            if out == F8:
+                assert torch.equal(y.values[-2:].view(torch.uint8), ordinary.values[-2:].view(torch.uint8))
+                assert torch.equal(y.scale[-2:], ordinary.scale[-2:])
+            else:
+                assert torch.equal(y[-2:], ordinary[-2:])
+
+
+@pytest.mark.parametrize("kind", ["tiny", "lowest"])
+def test_norm_of_special_rows(kind):
+    """What the norm makes of the rows of test_special_rows that hold numbers only."""
+    need_gpu()
+    x = _rows(5, 6, 700, 0, torch.float32)
+    if kind == "tiny":
+        x[2] = 2.0 ** -130
+    else:
+        x[2, 333] = torch.finfo(torch.float32).min
+    y, _ = p24.rms_norm(x, torch.ones(700, device="cuda"))
+    v, s = y.values.float()[2], y.scale[2].item()
+    if kind == "tiny":                                       # over sqrt(eps): 2^-130 1000, under the smallest scale
+        assert s == float(TINY) and (v > 0).all()
+    else:
+        top = 700 ** 0.5                                     # all of the mean square is one value
+        assert v[333] == -448 and not v[:333].any() and abs(s * 448 / top - 1) < 64 * U
+
+
+@pytest.mark.parametrize("out", [F8, torch.float32], ids=["f8", "f32"])
+@pytest.mark.parametrize("width", [65, 700, 2049, 8192, 16384, 40001])
+def test_norm_of_mixed_rows(width, out):
+    """Large, ordinary, small and no values in one row, in runs that fall to different threads; no eps."""
+    need_gpu()
+    x = _rows(71, 6, width, 0, torch.float32)
+    part = max(1, width // 5)
+    for row, powers in enumerate(([90, -60, 0], [-60, 90, -60], [0, -45, 62], [-50, -120, -42], [0, -60, -130], [120, -45, 30])):
+        for i, p in enumerate(powers):
+            x[row, i * part:(i + 1) * part] *= 2.0 ** p
+        x[row, 4 * part:] = 0
+    x.clamp_(-3e38, 3e38)
+    w = 1 + 0.1 * _rows(9, 1, width, 0, torch.float32)[0]
+    y, _ = p24.rms_norm(x, w, eps=0.0, out_dtype=out)
+    e = x.to(D) / torch.sqrt(x.to(D).square().mean(dim=1, keepdim=True)) * w.to(D)
+    _check_rows(y, e, 64 * U, out)
