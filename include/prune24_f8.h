@@ -109,6 +109,7 @@ P24_API p24_status prune24_decompress_f8(const void* data, const float* scale, i
  * spmm24_f8 -- for tokens n and output features m:
  *     Y[n][m] = act(w_scale[m] x_scale[n] sum_k W[m][k] X[n][k] + bias[m])
  *               + residual[n][m]
+ *   (the sum times x_scale, then times w_scale, in every kernel).
  *   data, w_scale   the compressed M x K weight; K % 64 == 0, K > 0.
  *   X         N x K e4m3, leading dimension ldx >= K, ldx % 16 == 0, 16 B
  *             aligned, 512 * ldx < 2^32; N <= 65535 * 32; M, K < 2^24

@@ -287,20 +287,21 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   // The residual of region r (wave r's output tile) on its way to LDS, in the
   // stages that the last steps leave free: RPS regions a stage, the stage of
   // "step" count + r / RPS.  A region is [token][16 B chunk c of its features], the
-  // chunks exchanged (f8_residual_vector) so that both the accumulators' order (one
+  // chunks exchanged (F8RReads) so that both the accumulators' order (one
   // feature quad of 32 tokens) and whole rows spread over the banks.
   const __amdgpu_buffer_rsrc_t r_rsrc =
       f8_rsrc((const uint8_t*)args.residual + ((int64_t)n0 * args.ldr + m0) * 2,
-              INPLACE && args.res_dma ? f8_residual_bytes<C>(n_rows, args.ldr, args.M - m0) : 0u);
+              INPLACE && args.res_dma ? F8RReads<C>::bytes(n_rows, args.ldr, args.M - m0) : 0u);
+  const F8RReads<C> r_reads(lane, wave, args.ldr);
   const int r_t = lane / C::CH;                                  // token of a lane in its load, 64 / CH a load
   auto issue_residual = [&](auto Q, int it, uint32_t st) {
     constexpr int q = decltype(Q)::value;
     const int l = q * LW + wave;                                 // load l of the stage, of its region l / RL
     const int r = (it - count) * C::RPS + l / C::RL;
     if (q < C::RDMA && r < C::GWAVES) {
-      int ln = lane;
-      asm volatile("" : "+v"(ln));   // the offsets of each load, too, are not kept over the loop
-      load_to_lds(r_rsrc, lds + st + l * 1024, f8_residual_vector<C>(ln, l, r, WGN, (uint32_t)args.ldr * 2), 0);
+      uint32_t rest = r_reads.uniform(l, r, WGN);
+      asm volatile("" : "+s"(rest));   // as for X
+      load_to_lds(r_rsrc, lds + st + l * 1024, r_reads.vector(rest), 0);
     } else if (it == count || it < NSTAGE) {
       issue(Q, it, st);     // until the last step has landed the waits count on a whole step's loads
     }
@@ -496,7 +497,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
           const int f = wm * C::WTM + 32 * i + 8 * q + 4 * h;
           const f32x4 w = *reinterpret_cast<const f32x4*>(sc + f);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) z[4 * q + u] = acc[i][j][4 * q + u] * (sx * w[u]);
+          for (int u = 0; u < 4; ++u) z[4 * q + u] = acc[i][j][4 * q + u] * sx * w[u];   // sx w alone can leave fp32
         }
         if (args.bias) {
 #pragma unroll

@@ -105,17 +105,25 @@ struct F8WReads {
   }
 };
 
-// The residual (bf16, rows of whole aligned 16 B chunks): load l of a stage is tokens
-// (l % RL) * 64 / CH on of region r, wave r's output tile; chunk c of a region's token t
-// goes to place c ^ (t % CH).
+// The residual (bf16, rows of whole aligned 16 B chunks): load l of a stage, by wave l % LW, is
+// tokens (l % RL) * 64 / CH on of region r, wave r's output tile; chunk c of a region's token t
+// goes to place c ^ (t % CH).  All of a wave's loads have the same t % CH in a lane: one
+// offset of its own and a uniform rest.
 template <class C>
-P24_HD uint32_t f8_residual_bytes(int rows, int64_t ldr, int features) {
-  return (uint32_t)((rows - 1) * ldr + features) * 2;
-}
-template <class C>
-P24_HD uint32_t f8_residual_vector(int lane, int l, int region, int WGN, uint32_t row_bytes) {
-  const int t = (l % C::RL) * (64 / C::CH) + lane / C::CH, chunk = (lane % C::CH) ^ (t % C::CH);
-  return (uint32_t)((region % WGN) * C::WTN + t) * row_bytes + (uint32_t)((region / WGN) * C::WTM + 8 * chunk) * 2;
-}
+struct F8RReads {
+  static_assert(C::LW * (64 / C::CH) % C::CH == 0 && (C::RL % C::LW == 0 || C::LW % C::RL == 0), "one t % CH a lane");
+  uint32_t voff, row_bytes;
+  int wave;
+  P24_HD F8RReads(int lane, int wave_, int64_t ldr) : row_bytes((uint32_t)ldr * 2), wave(wave_) {
+    const int t = (wave % C::RL) * (64 / C::CH) + lane / C::CH, chunk = (lane % C::CH) ^ (t % C::CH);
+    voff = (uint32_t)t * row_bytes + 16 * chunk;
+  }
+  static P24_HD uint32_t bytes(int rows, int64_t ldr, int features) { return (uint32_t)((rows - 1) * ldr + features) * 2; }
+  P24_HD uint32_t uniform(int l, int region, int WGN) const {
+    const int t = (region % WGN) * C::WTN + (l % C::RL - wave % C::RL) * (64 / C::CH);
+    return (uint32_t)t * row_bytes + (uint32_t)((region / WGN) * C::WTM) * 2;
+  }
+  P24_HD uint32_t vector(uint32_t uniform) const { return voff + uniform; }
+};
 
 }  // namespace p24

@@ -32,6 +32,7 @@ long f8_tile(int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldr) {
       for (int wave = 0; wave < LW; ++wave)
         for (int lane = 0; lane < 64; ++lane) {
           const F8XReads<C> x(lane, wave, ldx, (int)K);
+          const F8RReads<C> res(lane, wave, ldr);
           for (int64_t g = 0; g < nk; ++g) {
             for (int q = 0; q < C::X_DMA; ++q)
               n_bad += bad(x.vector(x.rows(q), g == nk - 1), x.scalar((int)g), 16, x.bytes(rows, ldx, (int)K), x_end);
@@ -43,8 +44,7 @@ long f8_tile(int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldr) {
               for (int r0 = 0; r0 < C::GWAVES; r0 += C::RPS) {
                 const int l = q * LW + wave, r = r0 + l / C::RL;
                 if (r < C::GWAVES)
-                  n_bad += bad(f8_residual_vector<C>(lane, l, r, WGN, (uint32_t)ldr * 2), 0, 16,
-                               f8_residual_bytes<C>(rows, ldr, (int)(M - m0)), r_end);
+                  n_bad += bad(res.vector(res.uniform(l, r, WGN)), 0, 16, res.bytes(rows, ldr, (int)(M - m0)), r_end);
               }
         }
     }

@@ -544,3 +544,20 @@ def test_norm_of_mixed_rows(width, out):
     y, _ = p24.rms_norm(x, w, eps=0.0, out_dtype=out)
     e = x.to(D) / torch.sqrt(x.to(D).square().mean(dim=1, keepdim=True)) * w.to(D)
     _check_rows(y, e, 64 * U, out)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tile", TILES)
+def test_product_of_scales_out_of_range(monkeypatch, tile, out):
+    """Scales whose product leaves fp32 while the result does not: tokens of 2^-118 against weights of 2^-10, and
+    tokens of 1e30 that meet only the zeros of weights of 1e15."""
+    need_gpu()
+    monkeypatch.setenv("P24_F8_TILE", tile)
+    M, N, K = 96, 70, 4096
+    c = p24.compress_f8(torch.full((M, K), 2.0 ** -10, device="cuda"))
+    Y = p24.spmm24_f8(c, p24.gated_act(torch.full((N, K), 2.0 ** -118, device="cuda"), act="none"), out_dtype=out)
+    assert ((Y.to(D) * 2.0 ** 117 - 1).abs() <= 4 * U).all()       # K / 2 products of 2^-128; whole numbers until the scales
+    W, x = torch.zeros(M, K, device="cuda"), torch.zeros(N, K, device="cuda")
+    W[:, 0::4], W[:, 1::4], x[:, 2::4], x[:, 3::4] = 1e15, -1e15, 1e30, 2e30
+    Y = p24.spmm24_f8(p24.compress_f8(W), p24.gated_act(x, act="none"), out_dtype=out)
+    assert (Y == 0).all()
