@@ -269,14 +269,20 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   const bool loader = wave < C::LW;
 
   // load Q of a loading wave for the group's step `it` (its last one past the end) into the stage at byte st
-  auto issue = [&](auto Q, int it, uint32_t st) {
+  // (WHOLE: no token of the tile lies past N, and the rows go into the scalar offset, which spares
+  // an addition a load: 8192^3 257 -> 254 us)
+  auto issue = [&](auto Q, int it, uint32_t st, auto WHOLE) {
     constexpr int q = decltype(Q)::value;
     uint8_t* stage = lds + st;
     const int g = k_first + min(it, count - 1);
     if constexpr (q < C::X_DMA) {
       uint32_t rows = x_reads.rows(q);
-      asm volatile("" : "+s"(rows));   // added here: kept over the loop, the loads' offsets would take a register each
-      load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, x_reads.vector(rows, g == nk - 1), x_reads.scalar(g));
+      if constexpr (decltype(WHOLE)::value) {
+        load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, x_reads.vector(0, g == nk - 1), x_reads.scalar(g) + rows);
+      } else {
+        asm volatile("" : "+s"(rows));   // added here: kept over the loop, the loads' offsets would take a register each
+        load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, x_reads.vector(rows, g == nk - 1), x_reads.scalar(g));
+      }
     } else {
       constexpr int j = q - C::X_DMA;
       if (C::A_LAST != 0 && j == C::A_DMA - 1 && !last_load) return;
@@ -303,7 +309,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
       asm volatile("" : "+s"(rest));   // as for X
       load_to_lds(r_rsrc, lds + st + l * 1024, r_reads.vector(rest), 0);
     } else if (it == count || it < NSTAGE) {
-      issue(Q, it, st);     // until the last step has landed the waits count on a whole step's loads
+      issue(Q, it, st, std::false_type{});     // until the last step has landed the waits count on a whole step's loads
     }
   };
 
@@ -351,7 +357,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   // The multiplies of one 64-k block, with the reads of the next one (block RSS
   // of the stage at byte rst) spread over their first three quarters and, where
   // LD, this wave's loads of step g into the stage at byte lst, one after each
-  // multiply (LD 1: operands, 2: the residual).
+  // multiply (LD 1: operands, 2: the residual, 3: operands of a tile with no token past N).
   auto block = [&](auto LD, const Frags& f, Frags& next, auto RSS, uint32_t rst, int g, uint32_t lst) {
     constexpr int NM = TM * TN, SPREAD = NM * 3 / 4 > 0 ? NM * 3 / 4 : 1;
     static_for<0, NM>([&](auto K) {
@@ -363,14 +369,16 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
         const i32x8 bv = __builtin_shufflevector(f.b[j][0], f.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
         acc[i][j] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(f.a[i], bv, acc[i][j], f.pos[i], 0, 0);
       }
-      if constexpr (decltype(LD)::value == 1 && k < C::DMA) issue(K, g, lst);
+      if constexpr (decltype(LD)::value == 1 && k < C::DMA) issue(K, g, lst, std::false_type{});
+      if constexpr (decltype(LD)::value == 3 && k < C::DMA) issue(K, g, lst, std::true_type{});
       if constexpr (decltype(LD)::value == 2 && k < C::DMA) issue_residual(K, g, lst);
       constexpr int lo = k < SPREAD ? NR * k / SPREAD : NR, hi = k < SPREAD ? NR * (k + 1) / SPREAD : NR;
       static_for<lo, hi>([&](auto R) { read_one(RSS, R, rst, next); });
       __builtin_amdgcn_sched_barrier(0);
     });
     static_for<NM < C::DMA ? NM : C::DMA, C::DMA>([&](auto Q) {
-      if constexpr (decltype(LD)::value == 1) issue(Q, g, lst);
+      if constexpr (decltype(LD)::value == 1) issue(Q, g, lst, std::false_type{});
+      if constexpr (decltype(LD)::value == 3) issue(Q, g, lst, std::true_type{});
       if constexpr (decltype(LD)::value == 2) issue_residual(Q, g, lst);
     });
   };
@@ -378,6 +386,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
   // until at most n steps' loads of this wave are in flight
   auto wait_steps = [&](auto N) {
     constexpr int n = decltype(N)::value;
@@ -401,7 +410,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
   for (int g = 0; g < NSTAGE; ++g)
     if (loader) {
       if (residual_dma && g >= count) static_for<0, C::DMA>([&](auto Q) { issue_residual(Q, g, g * C::STAGE); });
-      else static_for<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE); });
+      else static_for<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE, std::false_type{}); });
     }
   wait_steps(std::integral_constant<int, NSTAGE - 1>{});
   __builtin_amdgcn_s_barrier();
@@ -432,6 +441,9 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8(const F8Args ar
     const int plain = LD && residual_dma ? max(common - NSTAGE, 0) : common;
     uint32_t st = 0;
     int it = 0;
+    if constexpr (decltype(LD)::value)
+      if (n_rows == BN)
+        for (; it < plain; ++it) st = body(I3{}, it, st);
     for (; it < plain; ++it) st = body(LD, it, st);
     if constexpr (decltype(LD)::value && INPLACE)
       for (; it < common; ++it) st = body(I2{}, it, st);
