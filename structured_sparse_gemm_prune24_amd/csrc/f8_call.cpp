@@ -15,6 +15,7 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/prune24_f8.h"
@@ -99,13 +100,14 @@ PyObject* give(const at::Tensor& y, const at::Tensor& scale, const at::Tensor& h
   return out;
 }
 
-// No C++ exception leaves a function that Python calls.
+// No C++ exception leaves a function that Python calls: it becomes the one that torch's own calls
+// raise (an allocation's torch.OutOfMemoryError among them).
 template <typename F>
 PyObject* guarded(F&& f) {
   try {
     return f();
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

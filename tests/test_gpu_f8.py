@@ -561,3 +561,22 @@ def test_product_of_scales_out_of_range(monkeypatch, tile, out):
     W[:, 0::4], W[:, 1::4], x[:, 2::4], x[:, 3::4] = 1e15, -1e15, 1e30, 2e30
     Y = p24.spmm24_f8(p24.compress_f8(W), p24.gated_act(x, act="none"), out_dtype=out)
     assert (Y == 0).all()
+
+
+def test_out_of_memory_is_torchs():
+    """An output that does not fit raises torch.OutOfMemoryError, as torch's own calls and the calls with `out` do."""
+    need_gpu()
+    tokens, width = 1 << 14, 1 << 13
+    x, w, c = torch.zeros(tokens, width, dtype=torch.bfloat16, device="cuda"), torch.ones(width, device="cuda"), _weight(1, width, 64)
+    q = p24.gated_act(x[:, :64], act="none")
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (32 << 20)) / total)
+    try:
+        for call in (lambda: p24.rms_norm(x, w, out_dtype=torch.float32), lambda: p24.gated_act(x, out_dtype=torch.float32),
+                     lambda: p24.gated_act(x), lambda: p24.spmm24_f8(c, q)):
+            with pytest.raises(torch.OutOfMemoryError):
+                call()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert not p24.gated_act(x).values.view(torch.uint8).any()
