@@ -82,7 +82,11 @@ at::Tensor make_rows(int64_t tokens, int64_t width, int code, const at::Device& 
 
 void* stream_of(const at::Device& dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
-PyObject* none() { Py_RETURN_NONE; }
+// "not the plain form": a failed conversion of an argument leaves no error behind
+PyObject* none() {
+  PyErr_Clear();
+  Py_RETURN_NONE;
+}
 
 // (values, scale or None, h or None) as a tuple
 PyObject* give(const at::Tensor& y, const at::Tensor& scale, const at::Tensor& h) {

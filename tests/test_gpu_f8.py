@@ -580,3 +580,14 @@ def test_out_of_memory_is_torchs():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert not p24.gated_act(x).values.view(torch.uint8).any()
+
+
+def test_arguments_that_are_no_numbers():
+    """A weight whose sizes are no whole numbers is refused by the binding's checks."""
+    need_gpu()
+    import ctypes
+    c = _weight(1, 32, 64)
+    x = p24.gated_act(_rows(1, 4, 64, 0, torch.float32), act="none")
+    for M, K in ((32.0, 64), (32, "64"), (None, 64)):
+        with pytest.raises((TypeError, ValueError, ctypes.ArgumentError)):
+            p24.spmm24_f8(p24.Compressed24F8(c.data, c.scale, M, K), x)
