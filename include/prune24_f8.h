@@ -111,9 +111,9 @@ P24_API p24_status prune24_decompress_f8(const void* data, const float* scale, i
  *               + residual[n][m]
  *   (the sum times x_scale, then times w_scale, in every kernel).
  *   data, w_scale   the compressed M x K weight; K % 64 == 0, K > 0.
- *   X         N x K e4m3, leading dimension ldx >= K, ldx % 16 == 0, 16 B
- *             aligned, 512 * ldx < 2^32; N <= 65535 * 32; M, K < 2^24
- *             (else P24_ERR_UNSUPPORTED).
+ *   X         N x K e4m3, 16 B aligned, leading dimension ldx >= K; with more
+ *             than one token ldx % 16 == 0 and 512 * ldx < 2^32.
+ *             N <= 65535 * 32; M, K < 2^24 (else P24_ERR_UNSUPPORTED).
  *   x_scale   N fp32 values.
  *   Y         N x M, P24_F32 or P24_BF16 (round to nearest even), leading
  *             dimension ldy >= M, naturally aligned.

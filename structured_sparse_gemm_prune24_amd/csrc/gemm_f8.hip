@@ -770,6 +770,7 @@ extern "C" P24_API p24_status spmm24_f8(const void* data, const float* w_scale, 
   if (ldx < K || ldy < M || (residual && ldr < M)) return P24_ERR_SHAPE;
   if (K % 64) return P24_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return P24_OK;
+  if (N == 1) ldx = K;   // a single token has no stride of its own
   if (K == 0 || K >= (1 << 24) || M >= (1 << 24) || N > 65535 * 32 || (uint64_t)ldx * 512 >= (1ull << 32)) return P24_ERR_UNSUPPORTED;
   if (!data || !w_scale || !X || !x_scale || !Y) return P24_ERR_NULL;
   const size_t ye = y_dtype == P24_F32 ? 4 : 2;

@@ -94,6 +94,13 @@ def test_product_refusals(L, code, args):
                        v["b"], v["act"], v["r"], v["ldr"], None) == code
 
 
+def test_a_single_token_has_no_stride(L):
+    """One token's leading dimension passes the checks on it, and the call comes to its other arguments."""
+    for ldx in (72, 1 << 23):
+        many, one = (L.spmm24_f8(None, P, 32, 64, P, ldx, P, n, P, BF16, 32, None, 0, None, 0, None) for n in (2, 1))
+        assert one == NULL and many == (UNSUP if ldx == 1 << 23 else NULL)
+
+
 class _Dev:
     """A tensor's face for the binding's checks: a CPU tensor that says it is on the device."""
 

@@ -591,3 +591,19 @@ def test_arguments_that_are_no_numbers():
     for M, K in ((32.0, 64), (32, "64"), (None, 64)):
         with pytest.raises((TypeError, ValueError, ctypes.ArgumentError)):
             p24.spmm24_f8(p24.Compressed24F8(c.data, c.scale, M, K), x)
+
+
+def test_a_token_of_rows_at_any_stride():
+    """One token cut from a buffer whose rows are not 16 bytes apart."""
+    need_gpu()
+    for M, K in ((96, 64), (4096, 1024), (300, 192)):
+        c = _weight(1, M, K)
+        x = p24.gated_act(_rows(3, 1, K, 0, torch.float32), act="none")
+        for pad in (1, 8, 24):
+            buf = torch.zeros(3, K + pad, dtype=torch.uint8, device="cuda").view(F8)
+            row = buf[:1, :K]
+            row.copy_(x.values)
+            assert row.stride(0) % 16
+            want = p24.spmm24_f8(c, x)
+            assert torch.equal(p24.spmm24_f8(c, p24.Quantized8(row, x.scale)), want)
+            assert torch.equal(p24.spmm24_f8(c, p24.Quantized8(row, x.scale), out=torch.empty_like(want)), want)
