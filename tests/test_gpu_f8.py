@@ -607,3 +607,37 @@ def test_a_token_of_rows_at_any_stride():
             want = p24.spmm24_f8(c, x)
             assert torch.equal(p24.spmm24_f8(c, p24.Quantized8(row, x.scale)), want)
             assert torch.equal(p24.spmm24_f8(c, p24.Quantized8(row, x.scale), out=torch.empty_like(want)), want)
+
+
+@pytest.mark.parametrize("N,M,K", [(33, 65, 128), (70, 300, 192), (257, 260, 1024), (100, 136, 1088), (300, 513, 4160)])
+@pytest.mark.parametrize("tile", TILES)
+def test_integers_in_every_kernel(monkeypatch, tile, N, M, K):
+    """Small whole numbers through each kernel, both outputs: exact, whatever the order of the sums."""
+    need_gpu()
+    monkeypatch.setenv("P24_F8_TILE", tile)
+    rng = np.random.default_rng(N + K)
+    W = rng.integers(-6, 7, (M, K)).astype(np.float32)
+    W[:, 0] = 7                                       # the row's largest: scale 7 / 448 = 2^-6
+    c = p24.compress_f8(torch.from_numpy(W).cuda())
+    q = torch.from_numpy(rng.integers(-4, 5, (N, K)).astype(np.float32)).cuda().to(F8)
+    x = p24.Quantized8(q, torch.full((N,), 2.0, device="cuda"))
+    want = (2 * q.to(D)) @ p24.decompress_f8(c).to(D).T
+    r = torch.from_numpy(rng.integers(-64, 65, (N, M)).astype(np.float32)).cuda()
+    for out in (torch.float32, torch.bfloat16):
+        assert torch.equal(p24.spmm24_f8(c, x, out_dtype=out), want.to(out))
+        assert torch.equal(p24.spmm24_f8(c, x, out_dtype=out, residual=r.to(out)), (want + r.to(D)).to(out))
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,M,K", [(960, 1152, 2112), (957, 1145, 2112), (8640, 256, 2112), (8630, 248, 2112)])
+def test_one_group_of_waves_with_a_long_k(N, M, K, out):
+    """More than 256 tiles of 64 x 64 and of 128 x 64, where one group of waves walks a long K alone and the
+    residual takes over its stages."""
+    need_gpu()
+    c = _weight(M + K, M, K)
+    x = p24.gated_act(_rows(N, N, K, 0, torch.float32), act="none")
+    r, odd = _rows(5, N, M, 8, out), _rows(5, N, M, 9, out)
+    odd.copy_(r)
+    _check_product(c, x, out=out)
+    Y = _check_product(c, x, r=r, name="silu", out=out)
+    assert torch.equal(Y, p24.spmm24_f8(c, x, residual=odd, act="silu", out_dtype=out))
