@@ -662,9 +662,9 @@ static p24_status launch_tile(F8Args a, hipStream_t st) {
 
 // Which kernel.  A block tile's loads per multiply shrink with its size, but a
 // launch needs enough blocks for 256 CUs: the largest tile that still gives about
-// 144 of them wins.  Between 256 x 256 and 256 x 192 the rounds of blocks decide
-// (a round that fills every CU to the last is slower than its share: 2048 x 1024
-// with 6144 tokens, 192 blocks of 256 x 256 15.4, 256 of 256 x 192 23.6).
+// 144 of them wins.  Between 256 x 256 and 256 x 192 the rounds of blocks decide,
+// full ones included (2048 x 1024 with 6144 tokens, 256 blocks of 256 x 192 13.4,
+// 192 of 256 x 256 14.5; 4096 x 2048 with 6144 tokens, 512 blocks 33.5, 384 36.5).
 // Measured, us, M x K with N tokens:
 //   8192 x 8192, 8192   256x256 264, 256x128 358, 128x128 421
 //   2304 x 768, 4096    256x192 11.8 (198 blocks), 256x256 13.2 (144), 128x128 14.3
@@ -712,7 +712,7 @@ static F8Kernel choose_f8(const F8Args& a, bool exact) {
   if (!exact) {
     const int64_t n256 = f8_blocks(a, 256, 256), n192 = f8_blocks(a, 256, 192);
     const int64_t t256 = (n256 + 255) / 256 * 4, t192 = (n192 + 255) / 256 * 3;
-    if (n192 >= 160 && t192 < t256 && n192 % 256 != 0 && n192 % 256 <= 244) return F8Kernel::T256x192;
+    if (n192 >= 160 && t192 < t256) return F8Kernel::T256x192;
     if (n256 >= 144) return F8Kernel::T256x256;
   }
   if ((n128 >= 144 && n128 <= 256) || n128 >= 768) return F8Kernel::T256x128;

@@ -641,3 +641,12 @@ def test_one_group_of_waves_with_a_long_k(N, M, K, out):
     _check_product(c, x, out=out)
     Y = _check_product(c, x, r=r, name="silu", out=out)
     assert torch.equal(Y, p24.spmm24_f8(c, x, residual=odd, act="silu", out_dtype=out))
+
+
+@pytest.mark.parametrize("N,M,K", [(6144, 2048, 128), (6100, 2040, 192)])
+def test_a_full_round_of_blocks(N, M, K):
+    """256 blocks of 256 x 192, the library's own choice of kernel."""
+    need_gpu()
+    c = _weight(M + K, M, K)
+    x = p24.gated_act(_rows(N, N, K, 0, torch.float32), act="none")
+    _check_product(c, x, r=_rows(5, N, M, 8, torch.bfloat16), name="silu")
