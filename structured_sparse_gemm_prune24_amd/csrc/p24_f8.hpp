@@ -52,9 +52,11 @@ __device__ __forceinline__ float f8_scale(float amax) {
 // erfc(x) = erfcx(x) exp(-x^2), the smooth factor erfcx / 2 is t Q(t) with
 // t = 1 / (1 + p x), Q a least-squares fit at Chebyshev nodes reweighted to an even
 // relative error; the negative side has no cancellation.  For fp32 outputs
-// p = 0.45 and degree 9, error 3.3e-8; for bf16 and 8-bit ones, rounded by 2^-8 and
-// 2^-4 at most, p = 0.46 and degree 5, error 1.8e-5: an epilogue with little K under
+// p = 0.45 and degree 9, fit within 3.3e-8; for bf16 and 8-bit ones, rounded by 2^-8 and
+// 2^-4 at most, p = 0.46 and degree 5, fit within 1.8e-5: an epilogue with little K under
 // it is bound by these instructions (3106 x 128 with 7981 tokens 43.5 -> 36.8 us).
+// Beside the fit count the reciprocal and exp2 (one ulp each) and the rounding of
+// z^2 in the exponent: (1.5 z^2 + 40) 2^-24 of the result.
 template <bool F32>
 __device__ __forceinline__ float gelu_erfc(float z) {
   const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), F32 ? 0.3181980515339464f : 0.3252691193458121f, 1.0f));

@@ -9,7 +9,8 @@ residual's addition, gated activation, and the product with 2:4-sparse 8-bit wei
     y, h = p24.feed_forward_f8(x, r, g, w_gate_up, w_down)   # the four together
 
 Activations are tokens x features.  8-bit values are e4m3 with one fp32 scale per row.  As in the
-rest of the binding this is argument marshalling only.
+rest of the binding this is argument marshalling only, and the operators have no backward pass:
+they take tensors that require gradients, as they are, and return results without history.
 """
 from __future__ import annotations
 
@@ -125,7 +126,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=F8, out=None, h=None)
     x, residual [tokens, width] fp32 or bf16; weight fp32 [width].  y is a Quantized8 for
     out_dtype torch.float8_e4m3fn (the default), else a bf16 or fp32 tensor; h has x's dtype, and
     is None without a residual.  `out` (a Quantized8 or tensor) and `h` give the outputs' place;
-    h may be x or residual itself."""
+    h may be x or residual itself.  No gradients (inference only)."""
     if out is None and h is None and out_dtype in _CODES:
         got = (_CALL or _call()).norm(x, weight, residual, eps, _CODES[out_dtype])
         if got is not None:
@@ -161,7 +162,8 @@ def gated_act(gate, up=None, act="silu", out_dtype=F8, out=None):
 
     gate, up [tokens, width] fp32 or bf16, for instance the two halves of one product's output
     rows.  Returns a Quantized8 for out_dtype torch.float8_e4m3fn (the default), else a bf16 or
-    fp32 tensor; `out` gives its place.  With act "none" and no `up` it quantizes the rows."""
+    fp32 tensor; `out` gives its place.  With act "none" and no `up` it quantizes the rows.  No
+    gradients (inference only)."""
     if out is None and out_dtype in _CODES and act in _ACTS_F8:
         got = (_CALL or _call()).gate(gate, up, _ACTS_F8[act], _CODES[out_dtype])
         if got is not None:
@@ -222,7 +224,7 @@ def spmm24_f8(c: Compressed24F8, X: Quantized8, out_dtype=torch.bfloat16, out=No
 
     X.values [tokens, K] e4m3 (rows 16-byte aligned), X.scale fp32 [tokens]; bias fp32 [M];
     act "none", "relu", "gelu" or "silu"; residual [tokens, M] of the output's dtype, bf16 or
-    fp32, and may be `out` itself."""
+    fp32, and may be `out` itself.  No gradients (inference only)."""
     v = X.values
     if out is None and out_dtype in _STREAM_TYPES and act in _ACTS_F8:
         Y = (_CALL or _call()).product(c.data, c.scale, c.M, c.K, v, X.scale, _CODES[out_dtype], bias, _ACTS_F8[act],
@@ -259,7 +261,8 @@ def feed_forward_f8(x, residual, weight, w_gate_up: Compressed24F8, w_down: Comp
     """One feed-forward layer on 8-bit 2:4 weights: (y, h) with h = x + residual and
     y = W_down (act(gate) * up) + h, where gate and up are the halves of W_gate_up norm(h).
 
-    x, residual [tokens, width]; w_gate_up 2F x width, gate rows first; w_down width x F."""
+    x, residual [tokens, width]; w_gate_up 2F x width, gate rows first; w_down width x F.  No
+    gradients (inference only)."""
     if w_gate_up.M % 2 or w_gate_up.M // 2 != w_down.K or w_down.M != x.shape[-1]:
         raise ValueError(f"W_gate_up is {(w_gate_up.M, w_gate_up.K)}, W_down {(w_down.M, w_down.K)}: "
                          f"not 2F x {x.shape[-1]} and {x.shape[-1]} x F")
