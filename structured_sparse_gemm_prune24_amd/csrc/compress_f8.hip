@@ -120,6 +120,7 @@ static p24_status run_compress(const T* W, int64_t M, int64_t K, int64_t ldw, ui
                                hipStream_t st) {
   const int64_t steps = f8_steps(K), nblocks = f8_groups(M) * 4 * steps;
   hipLaunchKernelGGL(k_f8_scale<T>, dim3((unsigned)M), dim3(256), 0, st, W, ldw, (int)K, scale);
+  if (K == 0) return launch_status();   // rows of no values have their scales and nothing else
   hipLaunchKernelGGL(k_f8_compress<T>, dim3((unsigned)((nblocks + 3) / 4)), dim3(256), 0, st, W, ldw, M, (int)K, steps,
                      nblocks, scale, data);
   return launch_status();
@@ -149,8 +150,8 @@ extern "C" P24_API p24_status prune24_compress_f8(const void* W, int32_t w_dtype
   const p24_status s = check_mk(M, K);
   if (s != P24_OK) return s;
   if (ldw < K) return P24_ERR_SHAPE;
-  if (M == 0 || K == 0) return P24_OK;
-  if (!W || !data || !scale) return P24_ERR_NULL;
+  if (M == 0) return P24_OK;
+  if (!scale || (K > 0 && (!W || !data))) return P24_ERR_NULL;
   if (!aligned(W, w_dtype == P24_F32 ? 4 : 2) || !aligned(data, 16) || !aligned(scale, 4)) return P24_ERR_ALIGN;
   if (w_dtype == P24_F32)
     return run_compress((const float*)W, M, K, ldw, (uint8_t*)data, scale, (hipStream_t)stream);

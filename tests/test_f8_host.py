@@ -94,6 +94,11 @@ def test_product_refusals(L, code, args):
                        v["b"], v["act"], v["r"], v["ldr"], None) == code
 
 
+def test_rows_of_no_values_have_scales(L):
+    assert L.prune24_compress_f8(None, F32, 8, 0, 0, None, None, None) == NULL
+    assert L.prune24_compress_f8(None, F32, 0, 0, 0, None, None, None) == OK
+
+
 def test_a_single_token_has_no_stride(L):
     """One token's leading dimension passes the checks on it, and the call comes to its other arguments."""
     for ldx in (72, 1 << 23):

@@ -650,3 +650,13 @@ def test_a_full_round_of_blocks(N, M, K):
     c = _weight(M + K, M, K)
     x = p24.gated_act(_rows(N, N, K, 0, torch.float32), act="none")
     _check_product(c, x, r=_rows(5, N, M, 8, torch.bfloat16), name="silu")
+
+
+def test_compress_of_rows_without_values():
+    """K = 0: the scales of empty rows are the smallest, not memory as it was."""
+    need_gpu()
+    torch.full((5,), 7.0, device="cuda")              # what a fresh allocation would show
+    for dtype in (torch.float32, torch.bfloat16):
+        c = p24.compress_f8(torch.empty(5, 0, dtype=dtype, device="cuda"))
+        assert torch.equal(c.scale, torch.full((5,), float(TINY), device="cuda"))
+        assert c.data.numel() == 0 and tuple(p24.decompress_f8(c).shape) == (5, 0)
