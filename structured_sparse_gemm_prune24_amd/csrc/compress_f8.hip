@@ -1,5 +1,5 @@
 // Compression of 8-bit 2:4 weights and its inverse.  Run once when a weight is
-// loaded: bound by its two reads of W (8192 x 8192 fp32 109 us, 5 TB/s; 188 with a
+// loaded: bound by its two reads of W (8192 x 8192 fp32 92-109 us; 188 with a
 // lane per operand lane, whose loads stride by rows).
 #include "p24_api_internal.hpp"
 #include "p24_f8.hpp"
