@@ -31,6 +31,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("P24_LIBRARY") or os.path.join(PKG_DIR, "libprune24.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24.h")
 F8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24_f8.h")
+EXPERTS_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24_experts.h")
 
 # status codes / enums (mirror include/prune24.h)
 P24_OK = 0
@@ -125,6 +126,15 @@ _F8_SIGNATURES = {
     "spmm24_f8": (_c_i32, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i32, _c_i64, _c_vp,
                            _c_i32, _c_vp, _c_i64, _c_vp]),
 }
+# entry points declared in include/prune24_experts.h
+_EXPERTS_SIGNATURES = {
+    "experts_route": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i32, _c_vp, _c_i32, ctypes.c_float, _c_vp,
+                               _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "spmm24_f8_grouped": (_c_i32, [_c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64,
+                                   _c_vp, _c_i32, _c_i64, _c_vp, _c_i32, _c_vp]),
+    "experts_combine": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp,
+                                 _c_i32, _c_i64, _c_vp]),
+}
 
 _LIB = None
 
@@ -150,7 +160,7 @@ def lib() -> ctypes.CDLL:
         except ImportError:
             pass
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in {**_SIGNATURES, **_F8_SIGNATURES}.items():
+        for name, (res, args) in {**_SIGNATURES, **_F8_SIGNATURES, **_EXPERTS_SIGNATURES}.items():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
@@ -808,6 +818,8 @@ def gemm_bf16_xt(Wp, M: int, K: int, XT, out_dtype=None, out=None):
 
 
 # the 8-bit feed-forward operators need torch for their dtypes; the rest of the package imports it on use
+_EXPERTS_NAMES = ("Routing", "Experts24F8", "route", "compress_f8_experts", "spmm24_f8_grouped", "combine_experts",
+                  "feed_forward_f8_experts")
 _F8_NAMES = ("Quantized8", "Compressed24F8", "rms_norm", "gated_act", "compress_f8", "decompress_f8", "spmm24_f8",
              "feed_forward_f8")
 
@@ -816,6 +828,11 @@ def __getattr__(name):
     if name in _F8_NAMES:
         from . import f8
         value = getattr(f8, name)
+        globals()[name] = value
+        return value
+    if name in _EXPERTS_NAMES:
+        from . import experts
+        value = getattr(experts, name)
         globals()[name] = value
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,190 @@
+// spmm24_f8_grouped: the 8-bit 2:4 product of experts with ragged numbers of rows, on the tiles of
+// p24_f8_gemm.hpp.
+//
+// How many tiles there are is known on the device only.  Blocks of the block tiles walk over them
+// (as many as fit the chip at once, tile b, b + grid, ...), so that an upper bound of the tiles
+// costs nothing; a tile belongs to one expert, whose part of the operands it takes as a product of
+// its own.  The kernel for few rows has a block for every tile that there could be.
+#include <cstdlib>
+#include <cstring>
+
+#include "../../include/prune24_experts.h"
+#include "p24_api_internal.hpp"
+#include "p24_f8_gemm.hpp"
+
+namespace p24 {
+
+struct F8GroupedArgs {
+  F8Args a;          // of expert 0 and all rows
+  F8Groups groups;
+  int64_t w_bytes;   // of an expert's weight
+};
+
+// The part of one expert: rows first on, `count` of them.
+template <typename OutT>
+__device__ __forceinline__ F8Args f8_part(const F8GroupedArgs& g, int expert, int first, int count, F8RowMap& rows) {
+  F8Args a = g.a;
+  a.W += expert * g.w_bytes;
+  a.w_scale += (int64_t)expert * a.M;
+  if (a.bias) a.bias += (int64_t)expert * a.M;
+  a.Y = (OutT*)a.Y + first * a.ldy;
+  a.N = count;
+  a.residual = nullptr;
+  a.res_dma = 0;
+  rows.last = (uint32_t)g.groups.x_rows - 1;
+  rows.tokens = g.groups.tokens;
+  if (rows.tokens) {
+    rows.tokens += first;
+  } else {
+    a.X += first * a.ldx;
+    a.x_scale += first;
+  }
+  return a;
+}
+
+template <int W, typename OutT>
+__global__ __launch_bounds__(W * 64) void k_f8_tokens_grouped(const F8GroupedArgs g) {
+  int expert, first, count;
+  uint32_t first_tile;
+  F8GroupSearch<32> search(g.groups);
+  if (!search.find(blockIdx.y, expert, first, count, first_tile)) return;
+  F8RowMap rows;
+  const F8Args a = f8_part<OutT>(g, expert, first, count, rows);
+  f8_tokens_tile<W, OutT, true>(a, (int)(blockIdx.y - first_tile) * 32, rows);
+}
+
+template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
+__global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8_grouped(const F8GroupedArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[f8_lds_bytes<BM, BN, WGM, WGN, LW, KG, OutT>()];
+  const uint32_t nbm = g.a.nbm, tiles = F8GroupSearch<BN>(g.groups).total() * nbm;
+  for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+    const uint32_t b = xcd_remap(i, tiles);
+    int expert, first, count;
+    uint32_t first_tile, bm, bn;
+    F8GroupSearch<BN> search(g.groups);       // anew: its registers are the tile's
+    if (!search.find(b / nbm, expert, first, count, first_tile)) return;   // (never: b < tiles)
+    f8_place(b - first_tile * nbm, nbm, F8GroupSearch<BN>::tiles_of(count), bm, bn);
+    F8RowMap rows;
+    const F8Args a = f8_part<OutT>(g, expert, first, count, rows);
+    f8_block_tile<BM, BN, WGM, WGN, LW, KG, OutT, true>(a, lds, (int)bm * BM, (int)bn * BN, rows);
+    // the next tile's loads go where this one's epilogue reads
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+}
+
+// Most tiles of BN rows that `rows` rows of E experts can take: every expert with rows has one part tile at most.
+static int64_t f8_most_tiles(const F8GroupedArgs& g, int bn) {
+  const int64_t live = g.groups.experts < g.groups.rows ? g.groups.experts : g.groups.rows;
+  const int64_t most = (g.groups.rows - live) / bn + live;
+  return most;
+}
+
+template <int W, typename OutT>
+static p24_status launch_tokens_grouped(const F8GroupedArgs& g, hipStream_t st) {
+  const dim3 grid((unsigned)((g.a.M + 31) / 32), (unsigned)f8_most_tiles(g, 32));
+  if (grid.y > 65535) return P24_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL((k_f8_tokens_grouped<W, OutT>), grid, dim3(W * 64), 0, st, g);
+  return launch_status();
+}
+
+template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
+static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
+  g.a.nbm = (g.a.M + BM - 1) / BM;
+  const int64_t most = f8_most_tiles(g, BN) * g.a.nbm;
+  if (most >= (1ll << 31)) return P24_ERR_UNSUPPORTED;
+  // blocks that fit the 256 CUs at once; a multiple of the 8 XCDs
+  constexpr int LDS = f8_lds_bytes<BM, BN, WGM, WGN, LW, KG, OutT>();
+  const int64_t fit = 256 * (160 * 1024 / LDS < 4 ? 160 * 1024 / LDS : 4);
+  hipLaunchKernelGGL((k_gemm_f8_grouped<BM, BN, WGM, WGN, LW, KG, OutT>), dim3((unsigned)(most < fit ? most : fit)),
+                     dim3(WGM * WGN * KG * 64), 0, st, g);
+  return launch_status();
+}
+
+enum class F8GroupedKernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x192, T256x256 };
+
+static F8GroupedKernel choose_grouped(const F8GroupedArgs& g, bool exact) {
+  if (const char* e = getenv("P24_F8_TILE")) {
+    auto is = [&](const char* name) { return strcmp(e, name) == 0; };
+    if (is("tokens")) return F8GroupedKernel::TOKENS;
+    if (is("64x32")) return F8GroupedKernel::T64x32;
+    if (is("64x64")) return F8GroupedKernel::T64x64;
+    if (is("128x64")) return F8GroupedKernel::T128x64;
+    if (is("128x128")) return F8GroupedKernel::T128x128;
+    if (is("256x128") || (exact && (is("256x192") || is("256x256")))) return F8GroupedKernel::T256x128;
+    if (is("256x192")) return F8GroupedKernel::T256x192;
+    if (is("256x256")) return F8GroupedKernel::T256x256;
+  }
+  return F8GroupedKernel::T64x64;
+}
+
+template <typename OutT>
+static p24_status launch_grouped(const F8GroupedArgs& g, hipStream_t st) {
+  constexpr bool EXACT = sizeof(OutT) == 4;
+  switch (choose_grouped(g, EXACT)) {
+    case F8GroupedKernel::T256x256:
+      if constexpr (!EXACT) return launch_tile_grouped<256, 256, 2, 4, 8, 1, OutT>(g, st);
+    case F8GroupedKernel::T256x192:
+      if constexpr (!EXACT) return launch_tile_grouped<256, 192, 4, 2, 4, 1, OutT>(g, st);
+    case F8GroupedKernel::T256x128: return launch_tile_grouped<256, 128, 4, 2, 4, 1, OutT>(g, st);
+    case F8GroupedKernel::T128x128: return launch_tile_grouped<128, 128, 2, 4, 4, 1, OutT>(g, st);
+    case F8GroupedKernel::T128x64: return launch_tile_grouped<128, 64, 2, 2, 4, 1, OutT>(g, st);
+    case F8GroupedKernel::T64x64: return launch_tile_grouped<64, 64, 2, 2, 4, 1, OutT>(g, st);
+    case F8GroupedKernel::T64x32: return launch_tile_grouped<64, 32, 2, 1, 2, 1, OutT>(g, st);
+    case F8GroupedKernel::TOKENS: break;
+  }
+  if (g.a.K >= 1024) return launch_tokens_grouped<8, OutT>(g, st);
+  return launch_tokens_grouped<4, OutT>(g, st);
+}
+
+}  // namespace p24
+
+using namespace p24;
+
+extern "C" P24_API p24_status spmm24_f8_grouped(const void* data, const float* w_scale, int64_t E, int64_t M, int64_t K,
+                                                const void* X, int64_t ldx, const float* x_scale, int64_t x_rows,
+                                                const int32_t* offsets, const int32_t* tokens, int64_t rows, void* Y,
+                                                int32_t y_dtype, int64_t ldy, const float* bias, int32_t act,
+                                                void* stream) {
+  if (y_dtype != P24_F32 && y_dtype != P24_BF16) return P24_ERR_DTYPE;
+  if (!f8_act_known(act)) return P24_ERR_UNSUPPORTED;
+  if (E < 1 || M < 0 || K < 0 || rows < 0 || x_rows < 0 || M > INT32_MAX || K > INT32_MAX || rows > INT32_MAX ||
+      x_rows > INT32_MAX)
+    return P24_ERR_SHAPE;
+  if (ldx < K || ldy < M) return P24_ERR_SHAPE;
+  if (E > P24_EXPERTS_MAX || K % 64) return P24_ERR_UNSUPPORTED;
+  if (M == 0 || rows == 0) return P24_OK;
+  if (x_rows == 0 || (!tokens && x_rows != rows)) return P24_ERR_SHAPE;
+  if (x_rows == 1) ldx = K;   // a single row has no stride of its own
+  if (K == 0 || K >= (1 << 24) || M >= (1 << 24) || rows > 65535 * 32 || (uint64_t)ldx * 512 >= (1ull << 32)) return P24_ERR_UNSUPPORTED;
+  if (tokens && (ldx >= (1ll << 32) / x_rows)) return P24_ERR_UNSUPPORTED;
+  if (!data || !w_scale || !X || !x_scale || !Y || !offsets) return P24_ERR_NULL;
+  const size_t ye = y_dtype == P24_F32 ? 4 : 2;
+  if (!aligned(data, 16) || !aligned(X, 16) || ldx % 16 || !aligned(Y, ye) || !aligned(w_scale, 4) || !aligned(x_scale, 4) ||
+      !aligned(offsets, 4) || (tokens && !aligned(tokens, 4)) || (bias && !aligned(bias, 4)))
+    return P24_ERR_ALIGN;
+  F8GroupedArgs g{};
+  g.a.W = (const uint8_t*)data;
+  g.a.w_scale = w_scale;
+  g.a.X = (const uint8_t*)X;
+  g.a.x_scale = x_scale;
+  g.a.Y = Y;
+  g.a.bias = bias;
+  g.a.ldx = ldx;
+  g.a.ldy = ldy;
+  g.a.M = (int)M;
+  g.a.N = (int)rows;
+  g.a.K = (int)K;
+  g.a.act = act;
+  // an expert's rows start anywhere: whole lines if every row is
+  g.a.stream = aligned(Y, 128) && ldy * (int64_t)ye % 128 == 0 && (uint64_t)ldy * 1024 < (1ull << 32);
+  g.groups.offsets = offsets;
+  g.groups.tokens = tokens;
+  g.groups.experts = (int)E;
+  g.groups.rows = (int)rows;
+  g.groups.x_rows = (int)x_rows;
+  g.w_bytes = (int64_t)prune24_f8_bytes(M, K);
+  if (y_dtype == P24_F32) return launch_grouped<float>(g, (hipStream_t)stream);
+  return launch_grouped<uint16_t>(g, (hipStream_t)stream);
+}

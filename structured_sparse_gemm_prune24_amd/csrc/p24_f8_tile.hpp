@@ -65,10 +65,14 @@ struct F8Tile {
 template <class C>
 struct F8XReads {
   uint32_t voff, tail, jump;
+  // a lane's token in load q, and its 16 B chunk, the same in all loads
+  static P24_HD int row(int lane, int wave, int q) { return 8 * (q * C::LW + wave) + ((lane >> 3) ^ (wave & 1)); }
+  static P24_HD int chunk(int lane, int wave) { return (lane & 7) ^ (row(lane, wave, 0) & 7); }
+  static P24_HD uint32_t back(int chunk, int K) { return (K & 64) && chunk >= 4 ? 64 : 0; }   // in the last step
   P24_HD F8XReads(int lane, int wave, int64_t ldx, int K) {
-    const int row = 8 * wave + ((lane >> 3) ^ (wave & 1)), chunk = (lane & 7) ^ (row & 7);
-    voff = (uint32_t)(row * ldx + 16 * chunk);
-    tail = voff - ((K & 64) && chunk >= 4 ? 64 : 0);
+    const int c = chunk(lane, wave);
+    voff = (uint32_t)(row(lane, wave, 0) * ldx + 16 * c);
+    tail = voff - back(c, K);
     jump = (uint32_t)(8 * C::LW * ldx);
   }
   static P24_HD uint32_t bytes(int rows, int64_t ldx, int K) { return (uint32_t)((rows - 1) * ldx + K); }
