@@ -32,6 +32,7 @@ LIB_PATH = os.environ.get("P24_LIBRARY") or os.path.join(PKG_DIR, "libprune24.so
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24.h")
 F8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24_f8.h")
 EXPERTS_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24_experts.h")
+F8_BLOCK_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "prune24_f8_block.h")
 
 # status codes / enums (mirror include/prune24.h)
 P24_OK = 0
@@ -135,6 +136,14 @@ _EXPERTS_SIGNATURES = {
     "experts_combine": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp,
                                  _c_i32, _c_i64, _c_vp]),
 }
+# entry points declared in include/prune24_f8_block.h
+_F8_BLOCK_SIGNATURES = {
+    "quantize_f8_block": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_vp, _c_i64, _c_i32, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64,
+                                   _c_vp]),
+    "quantize_weight_f8_block": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]),
+    "gemm_f8_block": (_c_i32, [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i32,
+                               _c_i64, _c_vp, _c_i32, _c_vp, _c_i64, _c_vp]),
+}
 
 _LIB = None
 
@@ -160,7 +169,8 @@ def lib() -> ctypes.CDLL:
         except ImportError:
             pass
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in {**_SIGNATURES, **_F8_SIGNATURES, **_EXPERTS_SIGNATURES}.items():
+        for name, (res, args) in {**_SIGNATURES, **_F8_SIGNATURES, **_EXPERTS_SIGNATURES,
+                                  **_F8_BLOCK_SIGNATURES}.items():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
@@ -820,19 +830,21 @@ def gemm_bf16_xt(Wp, M: int, K: int, XT, out_dtype=None, out=None):
 # the 8-bit feed-forward operators need torch for their dtypes; the rest of the package imports it on use
 _EXPERTS_NAMES = ("Routing", "Experts24F8", "route", "compress_f8_experts", "spmm24_f8_grouped", "combine_experts",
                   "feed_forward_f8_experts")
+_F8_BLOCK_NAMES = ("Rows8Block", "Weight8Block", "quantize_f8_block", "quantize_weight_f8_block", "gemm_f8_block",
+                   "feed_forward_f8_block")
 _F8_NAMES = ("Quantized8", "Compressed24F8", "rms_norm", "gated_act", "compress_f8", "decompress_f8", "spmm24_f8",
              "feed_forward_f8")
 
 
 def __getattr__(name):
     if name in _F8_NAMES:
-        from . import f8
-        value = getattr(f8, name)
-        globals()[name] = value
-        return value
-    if name in _EXPERTS_NAMES:
-        from . import experts
-        value = getattr(experts, name)
-        globals()[name] = value
-        return value
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        from . import f8 as module
+    elif name in _EXPERTS_NAMES:
+        from . import experts as module
+    elif name in _F8_BLOCK_NAMES:
+        from . import f8_block as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = getattr(module, name)
+    globals()[name] = value
+    return value

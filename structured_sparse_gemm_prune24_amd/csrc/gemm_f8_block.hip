@@ -1,0 +1,587 @@
+// Y = act(sum_b sx[b][n] sw[m / 128][b] S_b + bias) + residual for dense 8-bit weights W (M x K)
+// and 8-bit activations X (N x K), S_b the sum over a block of 128 k, on the 8-bit MFMA
+// (v_mfma_f32_16x16x128_f8f6f4: 16 rows x 16 tokens x one whole block of k).
+//
+// One instruction makes one S_b of 16 x 16 outputs, from a zero accumulator; four
+// fused multiply-adds a lane scale it into the running sums, 16 cycles of the vector unit beside
+// 32 of the matrix unit.  In its result lane L holds token L % 16, rows 4 (L / 16) + [0, 4):
+// a lane's four values share one token, and a wave's rows one block of weights, so that the scale is
+// one number a lane for each 16 tokens and step.
+//
+// Operands: lane L takes row (token) L % 16 and 32 of the block's k, chunks L / 16 and 4 + L / 16 of 16 B.  Which k a
+// lane holds is free as long as both operands agree.
+#include <cstdlib>
+#include <cstring>
+#include <type_traits>
+
+#include "../../include/prune24_f8_block.h"
+#include "p24_api_internal.hpp"
+#include "p24_f8.hpp"
+#include "p24_f8b_tile.hpp"
+
+namespace p24 {
+
+struct F8BArgs {
+  const uint8_t* W;
+  const float* w_scale;
+  const uint8_t* X;
+  const float* x_scale;
+  void* Y;
+  const float* bias;
+  const void* residual;
+  int64_t ldw, ldx, ldxs, ldy, ldr;
+  int M, N, K;
+  int act;
+  int nbm, nbn;
+};
+
+typedef __attribute__((address_space(3))) void lds_void_b;
+
+template <int I, int N, typename F>
+__device__ __forceinline__ void steps_of(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    steps_of<I + 1, N>(f);
+  }
+}
+
+// 32 values of a row: two chunks of 16
+struct F8BFrag {
+  i32x4 c[2];
+};
+
+__device__ __forceinline__ bf16x8 widen_b(uint32_t v0, uint32_t v1) {
+  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v0, 1.0f, false);
+  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v0, 1.0f, true);
+  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v1, 1.0f, false);
+  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v1, 1.0f, true);
+  return (bf16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// Operands as the unit takes them: the 8 bits themselves, or (EXACT) widened to bf16.
+template <bool EXACT>
+struct F8BOperand;
+template <>
+struct F8BOperand<false> {
+  i32x8 v;
+  __device__ __forceinline__ void set(const F8BFrag& f) { v = __builtin_shufflevector(f.c[0], f.c[1], 0, 1, 2, 3, 4, 5, 6, 7); }
+};
+template <>
+struct F8BOperand<true> {
+  bf16x8 v[4];
+  __device__ __forceinline__ void set(const F8BFrag& f) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = widen_b((uint32_t)f.c[t / 2][2 * (t % 2)], (uint32_t)f.c[t / 2][2 * (t % 2) + 1]);
+  }
+};
+__device__ __forceinline__ f32x4 block_sum(const F8BOperand<false>& a, const F8BOperand<false>& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, (f32x4){}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 block_sum(const F8BOperand<true>& a, const F8BOperand<true>& b) {
+  f32x4 s = {};
+#pragma unroll
+  for (int t = 0; t < 4; ++t) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[t], b.v[t], s, 0, 0, 0);
+  return s;
+}
+
+// LDS reads are inline assembly, waited for by lgkmcnt: the compiler would hold
+// each one back until every direct-to-LDS load has landed.
+template <int OFF>
+__device__ __forceinline__ i32x4 lds_read16(uint32_t addr) {
+  i32x4 v;
+  asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ float lds_read4(uint32_t addr) {
+  float v;
+  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
+  return v;
+}
+__device__ __forceinline__ void tie(F8BFrag& f) {
+  asm volatile("" : "+v"(f.c[0]), "+v"(f.c[1]));
+}
+// until at most N of this wave's LDS reads are in flight
+template <int N>
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// f8_rsrc of a place that is the same in all lanes, and is known to be (else each load would loop over its values)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* p, uint32_t bytes) {
+  const uint64_t at = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  return f8_rsrc((const uint8_t*)(uintptr_t)((uint64_t)hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
+}
+
+template <int BM, int BN, int WGM, int WGN, int NST, typename OutT>
+__device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_t* lds) {
+  using C = F8BTile<BM, BN, WGM, WGN, NST>;
+  constexpr bool EXACT = sizeof(OutT) == 4;
+  constexpr int TM = C::TM, TN = C::TN, PAIRS = C::PAIRS;
+  typedef F8BOperand<EXACT> Operand;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WGN, wn = wave % WGN;
+
+  // block -> tile: each XCD a contiguous range, in groups of eight row blocks
+  const uint32_t b = xcd_remap(blockIdx.x, (uint32_t)args.nbm * args.nbn);
+  constexpr uint32_t GROUP = 8;
+  const uint32_t group_size = GROUP * args.nbn;
+  const uint32_t first_m = (b / group_size) * GROUP;
+  const uint32_t gsz = min((uint32_t)args.nbm - first_m, GROUP);
+  const int m0 = (int)__builtin_amdgcn_readfirstlane(first_m + (b % group_size) % gsz) * BM;
+  const int n0 = (int)__builtin_amdgcn_readfirstlane((b % group_size) / gsz) * BN;
+  const int m_rows = min(args.M - m0, BM), n_rows = min(args.N - n0, BN);
+
+  const F8BSteps steps(args.K);
+  const F8BReads<C::WAVES> x_reads(lane, wave, args.ldx, steps), w_reads(lane, wave, args.ldw, steps);
+  const F8BScaleReads<C> s_reads(lane, wave, n_rows, (m_rows + 127) / 128, args.ldxs, steps.count);
+  const __amdgpu_buffer_rsrc_t x_rsrc =
+      uniform_rsrc(args.X + (int64_t)n0 * args.ldx, F8BReads<C::WAVES>::bytes(n_rows, args.ldx, args.K));
+  const __amdgpu_buffer_rsrc_t w_rsrc =
+      uniform_rsrc(args.W + (int64_t)m0 * args.ldw, F8BReads<C::WAVES>::bytes(m_rows, args.ldw, args.K));
+  const int row_blocks = (args.M + 127) / 128;
+  const bool tokens_scales = wave < C::TOKEN_LOADS;
+  const float* scales = tokens_scales ? args.x_scale + n0 : args.w_scale + (int64_t)(m0 / 128) * steps.count;
+  const __amdgpu_buffer_rsrc_t s_rsrc =
+      uniform_rsrc(scales, (uint32_t)(tokens_scales ? (steps.count - 1) * args.ldxs + n_rows
+                                                    : min(row_blocks - m0 / 128, C::ROW_BLOCKS) * steps.count) * 4);
+
+  // load Q of this wave for step `it` into the stage at byte st
+  auto issue = [&](auto Q, int it, uint32_t st) {
+    constexpr int q = decltype(Q)::value;
+    const int block = steps.block(it);
+    const bool part = last_of(it, steps.count) == 0;
+    if constexpr (q < C::X_DMA) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(x_rsrc, (lds_void_b*)(lds + st + (q * C::WAVES + wave) * 1024), 16,
+                                               x_reads.vector(q, part), F8BReads<C::WAVES>::scalar(block), 0, 0);
+    } else if constexpr (q < C::X_DMA + C::W_DMA) {
+      constexpr int j = q - C::X_DMA;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rsrc, (lds_void_b*)(lds + st + C::X_BYTES + (j * C::WAVES + wave) * 1024), 16,
+                                               w_reads.vector(j, part), F8BReads<C::WAVES>::scalar(block), 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s_rsrc, (lds_void_b*)(lds + st + C::X_BYTES + C::W_BYTES + wave * 256), 4,
+                                               s_reads.voff, s_reads.scalar(block), 0, 0);
+    }
+  };
+
+  // LDS read addresses in stage 0: chunks L / 16 and 4 + L / 16 of row L % 16 of a 16-row tile
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_void_b*)lds;
+  const int r = lane & 15, c0 = lane >> 4;
+  const uint32_t in_tile = (uint32_t)((r ^ (r >> 3)) * 128);
+  uint32_t x_addr[2], w_addr[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t at = base + in_tile + (uint32_t)(((c0 + 4 * q) ^ (r & 7)) * 16);
+    x_addr[q] = at + wn * (C::WTN * 128);
+    w_addr[q] = at + C::X_BYTES + wm * (C::WTM * 128);
+  }
+  const uint32_t sx_addr = base + C::X_BYTES + C::W_BYTES + (wn * C::WTN + r) * 4;
+  const uint32_t sw_addr = base + C::X_BYTES + C::W_BYTES + C::TOKEN_LOADS * 256 + (wm * C::WTM / 128) * 4;
+
+  F8BFrag fa[2][2], fb[TN];       // rows: the pair in use and the next one; tokens
+  float sx[TN], sw, s[TN];        // the next step's scales as they lie in LDS; this step's products
+  f32x4 acc[TM][TN], sum[2][2];   // running sums; the block sums on their way into them
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = (f32x4){};
+
+  auto read_pair = [&](auto P, uint32_t st, F8BFrag (&f)[2]) {
+    constexpr int p = decltype(P)::value;
+    steps_of<0, 2>([&](auto I) {
+      constexpr int i = decltype(I)::value, off = (2 * p + i) * 2048;
+      f[i].c[0] = lds_read16<off>(w_addr[0] + st);
+      f[i].c[1] = lds_read16<off>(w_addr[1] + st);
+    });
+  };
+  auto read_tokens = [&](auto J, uint32_t st) {
+    constexpr int j = decltype(J)::value;
+    fb[j].c[0] = lds_read16<j * 2048>(x_addr[0] + st);
+    fb[j].c[1] = lds_read16<j * 2048>(x_addr[1] + st);
+  };
+  auto read_scales = [&](uint32_t st) {
+    sw = lds_read4<0>(sw_addr + st);
+    steps_of<0, TN>([&](auto J) { sx[decltype(J)::value] = lds_read4<decltype(J)::value * 64>(sx_addr + st); });
+  };
+  // the pair's block sums of token tile j into the running sums, one j behind the matrix unit
+  auto scale_in = [&](auto P, auto J) {
+    constexpr int p = decltype(P)::value, j = decltype(J)::value;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) acc[2 * p + i][j][u] = fmaf(sum[j & 1][i][u], s[j], acc[2 * p + i][j][u]);
+  };
+  using I0 = std::integral_constant<int, 0>;
+
+#pragma unroll
+  for (int g = 0; g < NST; ++g) steps_of<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE); });
+  wait_vm<(NST - 1) * C::DMA>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  if (steps.rest) {
+    // the first step's weights past K, whose tokens repeat chunk 0: zeros
+    for (int u = threadIdx.x; u < BM * 8; u += C::WAVES * 64) {
+      const int n = u >> 3, c = u & 7;
+      if (16 * c >= steps.rest)
+        *reinterpret_cast<u32x4*>(lds + C::X_BYTES + (n ^ ((n >> 3) & 1)) * 128 + ((c ^ (n & 7)) * 16)) = (u32x4){0, 0, 0, 0};
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+  read_scales(0);
+  read_pair(I0{}, 0, fa[0]);
+  steps_of<0, TN>([&](auto J) { read_tokens(J, 0); });
+
+  // Step `it` lives in stage it % NST.  Ahead of its last pair of row tiles, whose operands are in
+  // registers by then, every wave has read the stage and step it + 1 has landed: a barrier says so, the
+  // stage is refilled, and the next step's first operands are read under that pair's products.
+  auto step = [&](int it, uint32_t st) {
+    const uint32_t nx = st == (NST - 1) * C::STAGE ? 0 : st + C::STAGE;
+    steps_of<0, PAIRS>([&](auto P) {
+      constexpr int p = decltype(P)::value;
+      constexpr bool last = p == PAIRS - 1;
+      F8BFrag(&now)[2] = fa[p & 1];
+      F8BFrag(&next)[2] = fa[(p + 1) & 1];
+      if constexpr (p > 0) {
+        wait_lds<0>();
+        tie(now[0]);
+        tie(now[1]);
+      }
+      if constexpr (last) {
+        wait_vm<(NST - 2) * C::DMA>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        // every wave issues its loads over the pair's products
+      }
+      Operand a[2];
+      steps_of<0, TN>([&](auto J) {
+        constexpr int j = decltype(J)::value;
+        if constexpr (p == 0) {
+          // in flight behind tokens j: the later tokens, and the next pair once it has been asked for
+          wait_lds<2 * (TN - 1 - j) + (j > 0 ? 4 : 0)>();
+          if constexpr (j == 0) {
+            tie(now[0]);
+            tie(now[1]);
+            asm volatile("" : "+v"(sw));
+#pragma unroll
+            for (int v = 0; v < TN; ++v) asm volatile("" : "+v"(sx[v]));
+#pragma unroll
+            for (int v = 0; v < TN; ++v) s[v] = sx[v] * sw;
+          }
+          tie(fb[j]);
+        }
+        if constexpr (j == 0) {
+          a[0].set(now[0]);
+          a[1].set(now[1]);
+          if constexpr (!last) read_pair(std::integral_constant<int, p + 1>{}, st, next);
+          else {
+            read_scales(nx);
+            read_pair(I0{}, nx, next);
+          }
+        }
+        Operand t;
+        t.set(fb[j]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sum[j & 1][i] = block_sum(a[i], t);
+        if constexpr (last) {
+          read_tokens(J, nx);
+          constexpr int lo = C::DMA * j / TN, hi = C::DMA * (j + 1) / TN;
+          steps_of<lo, hi>([&](auto Q) { issue(Q, it + NST, st); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (j > 0) scale_in(P, std::integral_constant<int, j - 1>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      scale_in(P, std::integral_constant<int, TN - 1>{});
+    });
+    return nx;
+  };
+  // (the pairs alternate between two buffers: an odd number of them would end in the wrong one)
+  static_assert(PAIRS % 2 == 0, "the next step's first pair goes where the step expects it");
+  uint32_t st = 0;
+  for (int it = 0; it < steps.count; ++it) st = step(it, st);
+
+  wait_vm<0>();
+  wait_lds<0>();
+  steps_of<0, TN>([&](auto J) { tie(fb[decltype(J)::value]); });
+  tie(fa[0][0]);
+  tie(fa[0][1]);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
+  // Epilogue by slices of 16 tokens through LDS as fp32, so that a lane holds eight consecutive
+  // features of a token for bias, activation, residual and store, the same features for every token.
+  constexpr int LPT = C::WTM / 8, TPI = 64 / LPT, PASSES = 16 / TPI;      // lanes per token, tokens per pass, passes
+  float* part = reinterpret_cast<float*>(lds) + wave * 16 * C::PITCH;
+  const int m = m0 + wm * C::WTM + 8 * (lane % LPT), left = args.M - m;
+  float bs[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bs[i] = 0.0f;
+  if (args.bias) load_row<8>(args.bias + m, left, bs);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(bs[i]));
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int n_first = n0 + wn * C::WTN + 16 * j;
+    float z[8 * PASSES], res[PASSES][8];
+    if (args.residual) {
+#pragma unroll
+      for (int t = 0; t < PASSES; ++t) {
+        const int n = n_first + t * TPI + lane / LPT;
+        if constexpr (EXACT) {
+          float lo[4], hi[4];
+          load_row<4>((const float*)args.residual + (int64_t)n * args.ldr + m, n < args.N ? left : 0, lo);
+          load_row<4>((const float*)args.residual + (int64_t)n * args.ldr + m + 4, n < args.N ? left - 4 : 0, hi);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            res[t][i] = lo[i];
+            res[t][4 + i] = hi[i];
+          }
+        } else {
+          load_row<8>((const uint16_t*)args.residual + (int64_t)n * args.ldr + m, n < args.N ? left : 0, res[t]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) *reinterpret_cast<f32x4*>(part + r * C::PITCH + 16 * i + 4 * c0) = acc[i][j];
+#pragma unroll
+    for (int t = 0; t < PASSES; ++t) {
+      const float* row = part + (t * TPI + lane / LPT) * C::PITCH + 8 * (lane % LPT);
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(row), hi = *reinterpret_cast<const f32x4*>(row + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[8 * t + i] = (i < 4 ? lo[i] : hi[i - 4]) + bs[i];
+    }
+    f8_act<EXACT>(z, args.act);
+#pragma unroll
+    for (int t = 0; t < PASSES; ++t) {
+      const int n = n_first + t * TPI + lane / LPT;
+      if (n >= args.N) continue;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = args.residual ? z[8 * t + i] + res[t][i] : z[8 * t + i];
+      store_row<8>((OutT*)args.Y + (int64_t)n * args.ldy + m, left, v);
+    }
+  }
+}
+
+// (two waves a SIMD: with more registers the compiler would hand the block sums to the accumulation
+// registers, from where each goes back one by one)
+template <int BM, int BN, int WGM, int WGN, int NST, typename OutT>
+__global__ __launch_bounds__(WGM * WGN * 64, 2) void k_gemm_f8_block(const F8BArgs args) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * F8BTile<BM, BN, WGM, WGN, NST>::STAGE];
+  f8_block_scaled_tile<BM, BN, WGM, WGN, NST, OutT>(args, lds);
+}
+
+// Few tokens: a block has RT x 16 rows and TT x 16 tokens, and its W waves split K, wave w taking blocks of
+// scales w, w + W, ..., U of them on the way at a time straight from memory; the partial tiles meet in
+// LDS, summed in wave order.
+template <int W, int RT, int TT, typename OutT>
+__global__ __launch_bounds__(W * 64) void k_f8_block_tokens(const F8BArgs args) {
+  constexpr bool EXACT = sizeof(OutT) == 4;
+  constexpr int U = RT * TT > 2 ? 2 : 4, PITCH = RT * 16 + 4;
+  __shared__ __attribute__((aligned(16))) float part[W][TT * 16 * PITCH];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, c0 = lane >> 4;
+  const int m0 = blockIdx.x * (RT * 16), n0 = blockIdx.y * (TT * 16);
+  const int blocks = (args.K + 127) / 128;
+  const uint8_t* w[RT];
+  const uint8_t* x[TT];
+  const float* sx[TT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) w[i] = args.W + (int64_t)min(m0 + 16 * i + r, args.M - 1) * args.ldw + 16 * c0;
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int n = min(n0 + 16 * j + r, args.N - 1);
+    x[j] = args.X + (int64_t)n * args.ldx + 16 * c0;
+    sx[j] = args.x_scale + n;
+  }
+  const float* sw = args.w_scale + (int64_t)(m0 / 128) * blocks;
+
+  // the four features of a token that a thread finishes
+  constexpr int FINISH = TT * 16 * RT * 4;
+  const int tn = threadIdx.x / (RT * 4), tm = (threadIdx.x % (RT * 4)) * 4;
+  const int n = n0 + tn, m = m0 + tm;
+  static_assert(FINISH <= W * 64, "one quad of features a thread");
+  const bool finisher = (int)threadIdx.x < FINISH && n < args.N && m < args.M;
+  float bs[4] = {0, 0, 0, 0}, res[4] = {0, 0, 0, 0};
+  if (finisher) {
+    if (args.bias) load_row<4>(args.bias + m, args.M - m, bs);
+    if (args.residual) load_row<4>((const OutT*)args.residual + (int64_t)n * args.ldr + m, args.M - m, res);
+  }
+
+  f32x4 acc[RT][TT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){};
+  for (int s = wave; s < blocks; s += U * W) {
+    F8BFrag fa[U][RT], fb[U][TT];
+    float scale[U][TT], ws[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = s + u * W;
+      if (u > 0 && at >= blocks) continue;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool in = at * 128 + 16 * (c0 + 4 * q) < args.K;     // K's part of the block
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          fa[u][i].c[q] = (i32x4){0, 0, 0, 0};
+          if (in) fa[u][i].c[q] = *reinterpret_cast<const i32x4*>(w[i] + at * 128 + 64 * q);
+        }
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          fb[u][j].c[q] = (i32x4){0, 0, 0, 0};
+          if (in) fb[u][j].c[q] = *reinterpret_cast<const i32x4*>(x[j] + at * 128 + 64 * q);
+        }
+      }
+      ws[u] = sw[at];
+#pragma unroll
+      for (int j = 0; j < TT; ++j) scale[u][j] = sx[j][at * args.ldxs];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u > 0 && s + u * W >= blocks) continue;
+      F8BOperand<EXACT> a[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) a[i].set(fa[u][i]);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        F8BOperand<EXACT> t;
+        t.set(fb[u][j]);
+        const float f = scale[u][j] * ws[u];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const f32x4 sum = block_sum(a[i], t);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(sum[v], f, acc[i][j][v]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < TT; ++j)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) *reinterpret_cast<f32x4*>(&part[wave][(16 * j + r) * PITCH + 16 * i + 4 * c0]) = acc[i][j];
+  __syncthreads();
+  if (finisher) {
+    f32x4 sum = {};
+#pragma unroll
+    for (int v = 0; v < W; ++v) sum += *reinterpret_cast<const f32x4*>(&part[v][tn * PITCH + tm]);
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = sum[i] + bs[i];
+    f8_act<EXACT>(z, args.act);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] += res[i];
+    store_row<4>((OutT*)args.Y + (int64_t)n * args.ldy + m, args.M - m, z);
+  }
+}
+
+template <int W, int RT, int TT, typename OutT>
+static p24_status launch_block_tokens(const F8BArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)((a.M + RT * 16 - 1) / (RT * 16)), (unsigned)((a.N + TT * 16 - 1) / (TT * 16)));
+  hipLaunchKernelGGL((k_f8_block_tokens<W, RT, TT, OutT>), grid, dim3(W * 64), 0, st, a);
+  return launch_status();
+}
+
+template <int BM, int BN, int WGM, int WGN, int NST, typename OutT>
+static p24_status launch_block_tile(F8BArgs a, hipStream_t st) {
+  a.nbm = (a.M + BM - 1) / BM;
+  a.nbn = (a.N + BN - 1) / BN;
+  if ((int64_t)a.nbm * a.nbn * (WGM * WGN * 64) > UINT32_MAX) return P24_ERR_UNSUPPORTED;   // a grid's threads
+  hipLaunchKernelGGL((k_gemm_f8_block<BM, BN, WGM, WGN, NST, OutT>), dim3((unsigned)(a.nbm * a.nbn)), dim3(WGM * WGN * 64), 0,
+                     st, a);
+  return launch_status();
+}
+
+enum class F8BKernel { TOKENS, T64x64, T128x128, T256x128, T256x256 };
+
+static int64_t block_tiles(const F8BArgs& a, int bm, int bn) {
+  return ((a.M + (int64_t)bm - 1) / bm) * ((a.N + (int64_t)bn - 1) / bn);
+}
+
+static F8BKernel choose_block(const F8BArgs& a, bool exact) {
+  if (const char* e = getenv("P24_F8_TILE")) {
+    auto is = [&](const char* name) { return strcmp(e, name) == 0; };
+    if (is("tokens")) return F8BKernel::TOKENS;
+    if (is("64x64")) return F8BKernel::T64x64;
+    if (is("128x128")) return F8BKernel::T128x128;
+    if (is("256x128") || (exact && is("256x256"))) return F8BKernel::T256x128;
+    if (is("256x256")) return F8BKernel::T256x256;
+  }
+  if (a.N <= 32) return F8BKernel::TOKENS;
+  if (!exact && block_tiles(a, 256, 256) >= 144) return F8BKernel::T256x256;
+  if (block_tiles(a, 256, 128) >= 144) return F8BKernel::T256x128;
+  if (block_tiles(a, 128, 128) >= 144) return F8BKernel::T128x128;
+  return F8BKernel::T64x64;
+}
+
+template <typename OutT>
+static p24_status launch_block(const F8BArgs& a, hipStream_t st) {
+  constexpr bool EXACT = sizeof(OutT) == 4;
+  switch (choose_block(a, EXACT)) {
+    case F8BKernel::T256x256:
+      if constexpr (!EXACT) return launch_block_tile<256, 256, 2, 4, 2, OutT>(a, st);
+    case F8BKernel::T256x128: return launch_block_tile<256, 128, 4, 2, 3, OutT>(a, st);
+    case F8BKernel::T128x128: return launch_block_tile<128, 128, 2, 2, 2, OutT>(a, st);
+    case F8BKernel::T64x64: return launch_block_tile<64, 64, 1, 4, 3, OutT>(a, st);
+    case F8BKernel::TOKENS: break;
+  }
+  if (a.N <= 16) return launch_block_tokens<8, 1, 1, OutT>(a, st);
+  return launch_block_tokens<8, 1, 2, OutT>(a, st);
+}
+
+}  // namespace p24
+
+using namespace p24;
+
+extern "C" P24_API p24_status gemm_f8_block(const void* W, int64_t ldw, const float* w_scale, int64_t M, int64_t K,
+                                            const void* X, int64_t ldx, const float* x_scale, int64_t ldxs, int64_t N,
+                                            void* Y, int32_t y_dtype, int64_t ldy, const float* bias, int32_t act,
+                                            const void* residual, int64_t ldr, void* stream) {
+  if (y_dtype != P24_F32 && y_dtype != P24_BF16) return P24_ERR_DTYPE;
+  if (!f8_act_known(act)) return P24_ERR_UNSUPPORTED;
+  if (M < 0 || N < 0 || K < 0) return P24_ERR_SHAPE;
+  if (ldw < K || ldx < K || ldxs < N || ldy < M || (residual && ldr < M)) return P24_ERR_SHAPE;
+  if (K % 16) return P24_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return P24_OK;
+  if (N == 1) ldx = K;   // a single row has no stride of its own
+  if (M == 1) ldw = K;
+  if (K == 0 || K >= (1 << 24) || M >= (1 << 24) || N > 65535 * 16 || ldx >= (1 << 23) || ldw >= (1 << 23) ||
+      ldxs >= (1ll << 30) / ((K + 127) / 128) - 1)
+    return P24_ERR_UNSUPPORTED;
+  if (!W || !w_scale || !X || !x_scale || !Y) return P24_ERR_NULL;
+  const size_t ye = y_dtype == P24_F32 ? 4 : 2;
+  if (!aligned(W, 16) || !aligned(X, 16) || ldw % 16 || ldx % 16 || !aligned(Y, ye) || (residual && !aligned(residual, ye)) ||
+      !aligned(w_scale, 4) || !aligned(x_scale, 4) || (bias && !aligned(bias, 4)))
+    return P24_ERR_ALIGN;
+  F8BArgs a{};
+  a.W = (const uint8_t*)W;
+  a.w_scale = w_scale;
+  a.X = (const uint8_t*)X;
+  a.x_scale = x_scale;
+  a.Y = Y;
+  a.bias = bias;
+  a.residual = residual;
+  a.ldw = ldw;
+  a.ldx = ldx;
+  a.ldxs = ldxs;
+  a.ldy = ldy;
+  a.ldr = ldr;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.act = act;
+  if (y_dtype == P24_F32) return launch_block<float>(a, (hipStream_t)stream);
+  return launch_block<uint16_t>(a, (hipStream_t)stream);
+}
