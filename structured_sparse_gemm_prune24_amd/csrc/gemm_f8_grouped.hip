@@ -5,6 +5,7 @@
 // (as many as fit the chip at once, tile b, b + grid, ...), so that an upper bound of the tiles
 // costs nothing; a tile belongs to one expert, whose part of the operands it takes as a product of
 // its own.  The kernel for few rows has a block for every tile that there could be.
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 
@@ -102,7 +103,33 @@ static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
   return launch_status();
 }
 
+// Which kernel.  Where the rows lie is not known here: the experts' numbers of rows are taken as
+// exponentially distributed, so that an expert with a rows on average has 1 / (1 - exp(-BN / a)) tiles of BN rows.
+// A block tile takes a time that was measured with all CUs at work, us: `tile` once (first loads,
+// epilogue) and `step` for each 128 of K; the blocks come in rounds of 256.  The fewest microseconds win.
+// That ranks the kernels and is no forecast: decoding sizes are bound by the weights' bytes.
+// Measured, us (T tokens of k experts, of E with M x K):
+//   4096 of 8, 64 of 4096 x 2048   256x256 234, 256x192 249, 256x128 269, 128x128 320, 64x64 496
+//   1024 of 8, 64 of 4096 x 2048   256x192 102, 256x128 106, 128x128 117, 256x256 120
+//   256 of 8, 128 of 2048 x 2048   128x64 65, 256x128 68, 64x32 72, tokens 116
+//   64 of 4, 32 of 4096 x 4096     64x32 59, 128x64 59, 64x64 64, tokens 73
+// The kernel without shared operands starts sooner but reads each row once per 32 features:
+//   1 of 8, 128 of 2048 x 4096     tokens 9.1, 64x32 13.6
+//   8 of 8, 64 of 2048 x 2048      tokens 25.7, 64x32 22.2
+// Over 70 shapes drawn at random (both outputs) the choice is 4 % behind the fastest of the eight (geometric mean).
 enum class F8GroupedKernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x192, T256x256 };
+
+struct F8GroupedCost {
+  F8GroupedKernel kernel;
+  int bm, bn;
+  double tile, step;
+};
+constexpr F8GroupedCost GROUPED_COSTS[] = {
+    {F8GroupedKernel::T64x32, 64, 32, 1.27, 0.074},     {F8GroupedKernel::T64x64, 64, 64, 1.63, 0.126},
+    {F8GroupedKernel::T128x64, 128, 64, 3.26, 0.157},   {F8GroupedKernel::T128x128, 128, 128, 4.7, 0.263},
+    {F8GroupedKernel::T256x128, 256, 128, 6.5, 0.525},  {F8GroupedKernel::T256x192, 256, 192, 8.7, 0.65},
+    {F8GroupedKernel::T256x256, 256, 256, 8.8, 0.91},
+};
 
 static F8GroupedKernel choose_grouped(const F8GroupedArgs& g, bool exact) {
   if (const char* e = getenv("P24_F8_TILE")) {
@@ -116,7 +143,23 @@ static F8GroupedKernel choose_grouped(const F8GroupedArgs& g, bool exact) {
     if (is("256x192")) return F8GroupedKernel::T256x192;
     if (is("256x256")) return F8GroupedKernel::T256x256;
   }
-  return F8GroupedKernel::T64x64;
+  const double rows = g.groups.rows, experts = g.groups.experts;
+  const double live = experts * -expm1(-rows / experts), mean = rows / live;    // experts with rows, theirs on average
+  auto blocks = [&](int bm, int bn) { return live / -expm1(-bn / mean) * ((g.a.M + bm - 1) / bm); };
+  const double small = blocks(32, 32);
+  if (small <= 800 || (small <= 1500 && g.a.K <= 1408)) return F8GroupedKernel::TOKENS;
+  F8GroupedKernel best = F8GroupedKernel::T64x32;
+  double least = 1e300;
+  for (const F8GroupedCost& c : GROUPED_COSTS) {
+    if (exact && c.bn > 128) continue;    // widened operands do not fit their registers
+    const double b = blocks(c.bm, c.bn), rounds = b < 256 ? 1.0 : b / 256;
+    const double us = rounds * (c.tile + c.step * ((g.a.K + 127) / 128));
+    if (us < least) {
+      least = us;
+      best = c.kernel;
+    }
+  }
+  return best;
 }
 
 template <typename OutT>
@@ -134,6 +177,7 @@ static p24_status launch_grouped(const F8GroupedArgs& g, hipStream_t st) {
     case F8GroupedKernel::T64x32: return launch_tile_grouped<64, 32, 2, 1, 2, 1, OutT>(g, st);
     case F8GroupedKernel::TOKENS: break;
   }
+  if (g.a.K >= 2048 && ((int64_t)g.a.M + 31) / 32 * f8_most_tiles(g, 32) <= 256) return launch_tokens_grouped<16, OutT>(g, st);
   if (g.a.K >= 1024) return launch_tokens_grouped<8, OutT>(g, st);
   return launch_tokens_grouped<4, OutT>(g, st);
 }

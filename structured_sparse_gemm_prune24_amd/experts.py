@@ -20,7 +20,7 @@ from dataclasses import dataclass
 import torch
 
 from . import P24_ERR_SHAPE, P24_ERR_UNSUPPORTED, P24Error, _check, lib
-from .f8 import _CODES, _STREAM_TYPES, F8, Quantized8, _act_code, _rows, _vector, compress_f8, gated_act
+from .f8 import _ACTS_F8, _CODES, _STREAM_TYPES, F8, Quantized8, _act_code, _call, _rows, _vector, compress_f8, gated_act
 
 P24_SCORE_SOFTMAX, P24_SCORE_SIGMOID = 0, 1
 _SCORES = {"softmax": P24_SCORE_SOFTMAX, "sigmoid": P24_SCORE_SIGMOID}
@@ -46,6 +46,15 @@ class Experts24F8:
     K: int
 
 
+_CALL = None
+
+
+def _fast():
+    global _CALL
+    _CALL = _call()
+    return _CALL
+
+
 def _ints(t, name, shape, dev):
     if not t.is_cuda or t.device != dev:
         raise ValueError(f"{name} must be a device tensor on {dev}")
@@ -69,10 +78,14 @@ def route(logits, k: int, score="softmax", bias=None, normalize=True, scale=1.0)
     score "softmax" ranks by the logit and weighs by the softmax over the chosen experts (`normalize`)
     or over all; "sigmoid" ranks by sigmoid(logit) + bias (bias fp32 [E] or None) and weighs by the
     sigmoids, over their sum with `normalize`.  Ties go to the lower expert.  Weights times `scale`."""
+    code = _SCORES.get(score)
+    if code is not None and (bias is None or code == P24_SCORE_SIGMOID) and math.isfinite(scale):
+        got = (_CALL or _fast()).route(logits, k, code, bias, 1 if normalize else 0, scale)
+        if got is not None:
+            return Routing(*got)
     dev = logits.device
     ldl = _rows(logits, "logits", dev, _STREAM_TYPES)
     T, E = logits.shape
-    code = _SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
     if not 1 <= k <= E:
@@ -84,10 +97,11 @@ def route(logits, k: int, score="softmax", bias=None, normalize=True, scale=1.0)
     bp = None if bias is None else _vector(bias, "bias", E, dev)
     new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
     r = Routing(new(T, k), torch.empty((T, k), dtype=torch.float32, device=dev), new(E + 1), new(T * k), new(T, k))
-    _check(lib().experts_route(logits.data_ptr(), _CODES[logits.dtype], ldl, T, E, k, code, bp, int(bool(normalize)),
-                               scale, r.experts.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
-                               r.tokens.data_ptr(), r.positions.data_ptr(),
-                               torch.cuda.current_stream(dev).cuda_stream), "experts_route")
+    with torch.cuda.device(dev):
+        _check(lib().experts_route(logits.data_ptr(), _CODES[logits.dtype], ldl, T, E, k, code, bp, int(bool(normalize)),
+                                   scale, r.experts.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
+                                   r.tokens.data_ptr(), r.positions.data_ptr(),
+                                   torch.cuda.current_stream(dev).cuda_stream), "experts_route")
     return r
 
 
@@ -122,6 +136,11 @@ def spmm24_f8_grouped(c: Experts24F8, X: Quantized8, offsets, tokens=None, out_d
     each entry of `tokens` (of X without).  Rows behind the last expert's are not written: they keep what
     `out` held."""
     v = X.values
+    if out is None and out_dtype in _STREAM_TYPES and act in _ACTS_F8:
+        Y = (_CALL or _fast()).grouped(c.data, c.scale, c.E, c.M, c.K, v, X.scale, offsets, tokens, _CODES[out_dtype], bias,
+                                       _ACTS_F8[act])
+        if Y is not None:
+            return Y
     dev = v.device
     ldx = _rows(v, "X.values", dev, (F8,))
     n, K = v.shape
@@ -143,9 +162,10 @@ def spmm24_f8_grouped(c: Experts24F8, X: Quantized8, offsets, tokens=None, out_d
         ldy = c.M
     else:
         ldy = _rows(out, "out", dev, _STREAM_TYPES, (rows, c.M))
-    _check(lib().spmm24_f8_grouped(c.data.data_ptr(), ws, c.E, c.M, K, v.data_ptr(), ldx, xs, n, op, tp, rows,
-                                   out.data_ptr(), _CODES[out.dtype], ldy, bp, a,
-                                   torch.cuda.current_stream(dev).cuda_stream), "spmm24_f8_grouped")
+    with torch.cuda.device(dev):
+        _check(lib().spmm24_f8_grouped(c.data.data_ptr(), ws, c.E, c.M, K, v.data_ptr(), ldx, xs, n, op, tp, rows,
+                                       out.data_ptr(), _CODES[out.dtype], ldy, bp, a,
+                                       torch.cuda.current_stream(dev).cuda_stream), "spmm24_f8_grouped")
     return out
 
 
@@ -154,6 +174,10 @@ def combine_experts(Z, positions, weights, residual=None, out_dtype=None, out=No
 
     Z [rows, width] fp32 or bf16; positions int32, weights fp32 [tokens, k]; y has the residual's type,
     else Z's, unless out_dtype or `out` says otherwise; `out` may be the residual itself."""
+    if out is None and (out_dtype is None or out_dtype in _STREAM_TYPES):
+        y = (_CALL or _fast()).combine(Z, positions, weights, residual, -1 if out_dtype is None else _CODES[out_dtype])
+        if y is not None:
+            return y
     dev = Z.device
     ldz = _rows(Z, "Z", dev, _STREAM_TYPES)
     if positions.dim() != 2:
@@ -174,9 +198,10 @@ def combine_experts(Z, positions, weights, residual=None, out_dtype=None, out=No
     if residual is not None:
         ldr = _rows(residual, "residual", dev, (out.dtype,), shape)
         rp = residual.data_ptr()
-    _check(lib().experts_combine(Z.data_ptr(), _CODES[Z.dtype], ldz, Z.shape[0], pp, wp, T, k, shape[1], rp, ldr,
-                                 out.data_ptr(), _CODES[out.dtype], ldy, torch.cuda.current_stream(dev).cuda_stream),
-           "experts_combine")
+    with torch.cuda.device(dev):
+        _check(lib().experts_combine(Z.data_ptr(), _CODES[Z.dtype], ldz, Z.shape[0], pp, wp, T, k, shape[1], rp, ldr,
+                                     out.data_ptr(), _CODES[out.dtype], ldy, torch.cuda.current_stream(dev).cuda_stream),
+               "experts_combine")
     return out
 
 

@@ -17,7 +17,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _check, _w_code, lib
-from .f8 import _CODES, _STREAM_TYPES, F8, _act_code, _rows, _vector, rms_norm
+from .f8 import _ACTS_F8, _CODES, _STREAM_TYPES, F8, _act_code, _call, _rows, _vector, rms_norm
 
 
 @dataclass
@@ -32,6 +32,15 @@ class Weight8Block:
     """A dense M x K matrix in 8 bits: values[m, k] * scale[m // 128, k // 128]."""
     values: object       # torch.float8_e4m3fn [M, K]
     scale: object        # torch.float32 [ceil(M / 128), ceil(K / 128)]
+
+
+_CALL = None
+
+
+def _fast():
+    global _CALL
+    _CALL = _call()
+    return _CALL
 
 
 def _blocks(n):
@@ -57,6 +66,10 @@ def quantize_f8_block(x, up=None, act="none") -> Rows8Block:
 
     x, up [tokens, width] fp32 or bf16, for instance the two halves of one product's output rows; act
     "none", "relu", "gelu" or "silu".  No gradients (inference only)."""
+    if act in _ACTS_F8:
+        got = (_CALL or _fast()).quantize(x, up, _ACTS_F8[act])
+        if got is not None:
+            return Rows8Block(*got)
     dev = x.device
     ldx = _rows(x, "x", dev, _STREAM_TYPES)
     shape = tuple(x.shape)
@@ -69,9 +82,10 @@ def quantize_f8_block(x, up=None, act="none") -> Rows8Block:
         upp = up.data_ptr()
     values = _aligned_rows(shape, dev)
     scale = torch.empty((_blocks(shape[1]), shape[0]), dtype=torch.float32, device=dev)
-    _check(lib().quantize_f8_block(x.data_ptr(), _CODES[x.dtype], ldx, upp, ldu, a, shape[0], shape[1], values.data_ptr(),
-                                   values.stride(0), scale.data_ptr(), shape[0],
-                                   torch.cuda.current_stream(dev).cuda_stream), "quantize_f8_block")
+    with torch.cuda.device(dev):
+        _check(lib().quantize_f8_block(x.data_ptr(), _CODES[x.dtype], ldx, upp, ldu, a, shape[0], shape[1],
+                                       values.data_ptr(), values.stride(0), scale.data_ptr(), shape[0],
+                                       torch.cuda.current_stream(dev).cuda_stream), "quantize_f8_block")
     return Rows8Block(values, scale)
 
 
@@ -82,9 +96,10 @@ def quantize_weight_f8_block(W) -> Weight8Block:
     M, K = W.shape
     values = _aligned_rows((M, K), dev)
     scale = torch.empty((_blocks(M), _blocks(K)), dtype=torch.float32, device=dev)
-    _check(lib().quantize_weight_f8_block(W.data_ptr(), _w_code(W), M, K, ldw, values.data_ptr(), values.stride(0),
-                                          scale.data_ptr(), torch.cuda.current_stream(dev).cuda_stream),
-           "quantize_weight_f8_block")
+    with torch.cuda.device(dev):
+        _check(lib().quantize_weight_f8_block(W.data_ptr(), _w_code(W), M, K, ldw, values.data_ptr(), values.stride(0),
+                                              scale.data_ptr(), torch.cuda.current_stream(dev).cuda_stream),
+               "quantize_weight_f8_block")
     return Weight8Block(values, scale)
 
 
@@ -95,6 +110,10 @@ def gemm_f8_block(w: Weight8Block, X: Rows8Block, out_dtype=torch.bfloat16, out=
     "gelu" or "silu"; residual [tokens, M] of the output's dtype, bf16 or fp32, and may be `out` itself.  No
     gradients (inference only)."""
     v = X.values
+    if out is None and out_dtype in _STREAM_TYPES and act in _ACTS_F8:
+        Y = (_CALL or _fast()).block_product(w.values, w.scale, v, X.scale, _CODES[out_dtype], bias, _ACTS_F8[act], residual)
+        if Y is not None:
+            return Y
     dev = v.device
     ldx = _rows(v, "X.values", dev, (F8,))
     N, K = v.shape
@@ -120,9 +139,10 @@ def gemm_f8_block(w: Weight8Block, X: Rows8Block, out_dtype=torch.bfloat16, out=
     if residual is not None:
         ldr = _rows(residual, "residual", dev, (out.dtype,), shape)
         rp = residual.data_ptr()
-    _check(lib().gemm_f8_block(w.values.data_ptr(), ldw, w.scale.data_ptr(), M, K, v.data_ptr(), ldx, X.scale.data_ptr(),
-                               ldxs, N, out.data_ptr(), _CODES[out.dtype], ldy, bp, a, rp, ldr,
-                               torch.cuda.current_stream(dev).cuda_stream), "gemm_f8_block")
+    with torch.cuda.device(dev):
+        _check(lib().gemm_f8_block(w.values.data_ptr(), ldw, w.scale.data_ptr(), M, K, v.data_ptr(), ldx,
+                                   X.scale.data_ptr(), ldxs, N, out.data_ptr(), _CODES[out.dtype], ldy, bp, a, rp, ldr,
+                                   torch.cuda.current_stream(dev).cuda_stream), "gemm_f8_block")
     return out
 
 
