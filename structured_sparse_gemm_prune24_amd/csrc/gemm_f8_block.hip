@@ -8,8 +8,8 @@
 // a lane's four values share one token, and a wave's rows one block of weights, so that the scale is
 // one number a lane for each 16 tokens and step.
 //
-// Operands: lane L takes row (token) L % 16 and 32 of the block's k, chunks L / 16 and 4 + L / 16 of 16 B.  Which k a
-// lane holds is free as long as both operands agree.
+// Operands: lane L takes row (token) L % 16 and 32 of the block's k, two chunks of 16 B.  Which k a lane holds is
+// free as long as both operands agree.
 #include <cstdlib>
 #include <cstring>
 #include <type_traits>
@@ -171,14 +171,16 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
     }
   };
 
-  // LDS read addresses in stage 0: chunks L / 16 and 4 + L / 16 of row L % 16 of a 16-row tile
+  // LDS read addresses in stage 0: chunks 2 (L / 16) and one on of row L % 16 of a 16-row tile.  Sixteen lanes read
+  // at a time, half of them of the next lane group: with chunk L / 16 there they met on the same banks
+  // (8192^3 475 -> XXX us).
   const uint32_t base = (uint32_t)(uintptr_t)(lds_void_b*)lds;
   const int r = lane & 15, c0 = lane >> 4;
   const uint32_t in_tile = (uint32_t)((r ^ (r >> 3)) * 128);
   uint32_t x_addr[2], w_addr[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const uint32_t at = base + in_tile + (uint32_t)(((c0 + 4 * q) ^ (r & 7)) * 16);
+    const uint32_t at = base + in_tile + (uint32_t)(((2 * c0 + q) ^ (r & 7)) * 16);
     x_addr[q] = at + wn * (C::WTN * 128);
     w_addr[q] = at + C::X_BYTES + wm * (C::WTM * 128);
   }
@@ -188,6 +190,9 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   F8BFrag fa[2][2], fb[TN];       // rows: the pair in use and the next one; tokens
   float sx[TN], sw, s[TN];        // the next step's scales as they lie in LDS; this step's products
   f32x4 acc[TM][TN], sum[2][2];   // running sums; the block sums on their way into them
+#pragma unroll
+  for (int i = 0; i < 2; ++i) sum[0][i] = sum[1][i] = (f32x4){};
+  s[TN - 1] = 0.0f;
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -210,13 +215,15 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
     sw = lds_read4<0>(sw_addr + st);
     steps_of<0, TN>([&](auto J) { sx[decltype(J)::value] = lds_read4<decltype(J)::value * 64>(sx_addr + st); });
   };
-  // the pair's block sums of token tile j into the running sums, one j behind the matrix unit
-  auto scale_in = [&](auto P, auto J) {
-    constexpr int p = decltype(P)::value, j = decltype(J)::value;
+  // Group g of a step is token tile g % TN of pair g / TN.  Its block sums go into the running sums one group behind
+  // the matrix unit, the last group's in the next step (the first step finds zeros).
+  constexpr int GROUPS = PAIRS * TN;
+  auto scale_in = [&](auto G) {
+    constexpr int g = decltype(G)::value, p = g / TN, j = g % TN;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) acc[2 * p + i][j][u] = fmaf(sum[j & 1][i][u], s[j], acc[2 * p + i][j][u]);
+      for (int u = 0; u < 4; ++u) acc[2 * p + i][j][u] = fmaf(sum[g & 1][i][u], s[j], acc[2 * p + i][j][u]);
   };
   using I0 = std::integral_constant<int, 0>;
 
@@ -274,8 +281,6 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
             asm volatile("" : "+v"(sw));
 #pragma unroll
             for (int v = 0; v < TN; ++v) asm volatile("" : "+v"(sx[v]));
-#pragma unroll
-            for (int v = 0; v < TN; ++v) s[v] = sx[v] * sw;
           }
           tie(fb[j]);
         }
@@ -291,24 +296,24 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
         Operand t;
         t.set(fb[j]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sum[j & 1][i] = block_sum(a[i], t);
+        for (int i = 0; i < 2; ++i) sum[(p * TN + j) & 1][i] = block_sum(a[i], t);
         if constexpr (last) {
           read_tokens(J, nx);
           constexpr int lo = C::DMA * j / TN, hi = C::DMA * (j + 1) / TN;
           steps_of<lo, hi>([&](auto Q) { issue(Q, it + NST, st); });
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (j > 0) scale_in(P, std::integral_constant<int, j - 1>{});
+        scale_in(std::integral_constant<int, (p * TN + j + GROUPS - 1) % GROUPS>{});
+        if constexpr (p == 0) s[j] = sx[j] * sw;       // the step's scale, ahead of its first use
         __builtin_amdgcn_sched_barrier(0);
       });
-      scale_in(P, std::integral_constant<int, TN - 1>{});
     });
     return nx;
   };
-  // (the pairs alternate between two buffers: an odd number of them would end in the wrong one)
-  static_assert(PAIRS % 2 == 0, "the next step's first pair goes where the step expects it");
+  static_assert(PAIRS % 2 == 0, "pairs and groups alternate between two buffers: a step ends where the next expects it");
   uint32_t st = 0;
   for (int it = 0; it < steps.count; ++it) st = step(it, st);
+  scale_in(std::integral_constant<int, GROUPS - 1>{});
 
   wait_vm<0>();
   wait_lds<0>();
