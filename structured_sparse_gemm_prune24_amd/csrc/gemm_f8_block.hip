@@ -33,6 +33,7 @@ struct F8BArgs {
   int M, N, K;
   int act;
   int nbm, nbn;
+  int stream;     // the output's rows are whole cache lines
 };
 
 typedef __attribute__((address_space(3))) void lds_void_b;
@@ -118,9 +119,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* p, ui
   return f8_rsrc((const uint8_t*)(uintptr_t)((uint64_t)hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
 }
 
-template <int BM, int BN, int WGM, int WGN, int NST, typename OutT>
+template <int BM, int BN, int WGM, int WGN, int LW, int NST, int SPAN, typename OutT>
 __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_t* lds) {
-  using C = F8BTile<BM, BN, WGM, WGN, NST>;
+  using C = F8BTile<BM, BN, WGM, WGN, LW, NST>;
   constexpr bool EXACT = sizeof(OutT) == 4;
   constexpr int TM = C::TM, TN = C::TN, PAIRS = C::PAIRS;
   typedef F8BOperand<EXACT> Operand;
@@ -140,18 +141,21 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   const int m_rows = min(args.M - m0, BM), n_rows = min(args.N - n0, BN);
 
   const F8BSteps steps(args.K);
-  const F8BReads<C::WAVES> x_reads(lane, wave, args.ldx, steps), w_reads(lane, wave, args.ldw, steps);
-  const F8BScaleReads<C> s_reads(lane, wave, n_rows, (m_rows + 127) / 128, args.ldxs, steps.count);
+  const F8BReads<LW> x_reads(lane, wave, args.ldx, steps), w_reads(lane, wave, args.ldw, steps);
   const __amdgpu_buffer_rsrc_t x_rsrc =
-      uniform_rsrc(args.X + (int64_t)n0 * args.ldx, F8BReads<C::WAVES>::bytes(n_rows, args.ldx, args.K));
+      uniform_rsrc(args.X + (int64_t)n0 * args.ldx, F8BReads<LW>::bytes(n_rows, args.ldx, args.K));
   const __amdgpu_buffer_rsrc_t w_rsrc =
-      uniform_rsrc(args.W + (int64_t)m0 * args.ldw, F8BReads<C::WAVES>::bytes(m_rows, args.ldw, args.K));
-  const int row_blocks = (args.M + 127) / 128;
-  const bool tokens_scales = wave < C::TOKEN_LOADS;
-  const float* scales = tokens_scales ? args.x_scale + n0 : args.w_scale + (int64_t)(m0 / 128) * steps.count;
-  const __amdgpu_buffer_rsrc_t s_rsrc =
-      uniform_rsrc(scales, (uint32_t)(tokens_scales ? (steps.count - 1) * args.ldxs + n_rows
-                                                    : min(row_blocks - m0 / 128, C::ROW_BLOCKS) * steps.count) * 4);
+      uniform_rsrc(args.W + (int64_t)m0 * args.ldw, F8BReads<LW>::bytes(m_rows, args.ldw, args.K));
+  const int row_blocks = min((args.M + 127) / 128 - m0 / 128, C::ROW_BLOCKS);
+  const __amdgpu_buffer_rsrc_t sx_rsrc =
+      uniform_rsrc(args.x_scale + n0, (uint32_t)((steps.count - 1) * args.ldxs + n_rows) * 4);
+  const __amdgpu_buffer_rsrc_t sw_rsrc =
+      uniform_rsrc(args.w_scale + (int64_t)(m0 / 128) * steps.count, (uint32_t)(row_blocks * steps.count) * 4);
+  uint32_t s_voff[C::S_DMA];
+#pragma unroll
+  for (int q = 0; q < C::S_DMA; ++q)
+    s_voff[q] = F8BScaleReads<C>::vector(lane, F8BScaleReads<C>::number(wave, q), n_rows, row_blocks, steps.count);
+  const bool loader = LW == C::WAVES || wave < LW;
 
   // load Q of this wave for step `it` into the stage at byte st
   auto issue = [&](auto Q, int it, uint32_t st) {
@@ -159,15 +163,21 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
     const int block = steps.block(it);
     const bool part = last_of(it, steps.count) == 0;
     if constexpr (q < C::X_DMA) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(x_rsrc, (lds_void_b*)(lds + st + (q * C::WAVES + wave) * 1024), 16,
-                                               x_reads.vector(q, part), F8BReads<C::WAVES>::scalar(block), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(x_rsrc, (lds_void_b*)(lds + st + (q * LW + wave) * 1024), 16,
+                                               x_reads.vector(q, part), F8BReads<LW>::scalar(block), 0, 0);
     } else if constexpr (q < C::X_DMA + C::W_DMA) {
       constexpr int j = q - C::X_DMA;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rsrc, (lds_void_b*)(lds + st + C::X_BYTES + (j * C::WAVES + wave) * 1024), 16,
-                                               w_reads.vector(j, part), F8BReads<C::WAVES>::scalar(block), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rsrc, (lds_void_b*)(lds + st + C::X_BYTES + (j * LW + wave) * 1024), 16,
+                                               w_reads.vector(j, part), F8BReads<LW>::scalar(block), 0, 0);
     } else {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(s_rsrc, (lds_void_b*)(lds + st + C::X_BYTES + C::W_BYTES + wave * 256), 4,
-                                               s_reads.voff, s_reads.scalar(block), 0, 0);
+      constexpr int j = q - C::X_DMA - C::W_DMA;
+      const int number = F8BScaleReads<C>::number(wave, j);
+      void* to = lds + st + C::X_BYTES + C::W_BYTES + number * 256;
+      const uint32_t at = F8BScaleReads<C>::scalar(number, block, args.ldxs);
+      if (F8BScaleReads<C>::tokens(number))
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sx_rsrc, (lds_void_b*)to, 4, s_voff[j], at, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sw_rsrc, (lds_void_b*)to, 4, s_voff[j], at, 0, 0);
     }
   };
 
@@ -227,9 +237,15 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   };
   using I0 = std::integral_constant<int, 0>;
 
+  // A stage's refill goes out over SPAN groups: from the last pair of the step that read it into the next step.
+  constexpr int EARLY = C::DMA * (SPAN < TN ? SPAN : TN) / SPAN;      // its loads under that last pair
+  static_assert(SPAN >= 1 && SPAN <= GROUPS, "the refill has gone out before the next one starts");
+  if (loader) {
 #pragma unroll
-  for (int g = 0; g < NST; ++g) steps_of<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE); });
-  wait_vm<(NST - 1) * C::DMA>();
+    for (int g = 0; g < NST - 1; ++g) steps_of<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE); });
+    steps_of<0, EARLY>([&](auto Q) { issue(Q, NST - 1, (NST - 1) * C::STAGE); });
+    wait_vm<(NST - 2) * C::DMA + EARLY>();
+  }
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   if (steps.rest) {
@@ -250,8 +266,8 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   // Step `it` lives in stage it % NST.  Ahead of its last pair of row tiles, whose operands are in
   // registers by then, every wave has read the stage and step it + 1 has landed: a barrier says so, the
   // stage is refilled, and the next step's first operands are read under that pair's products.
-  auto step = [&](int it, uint32_t st) {
-    const uint32_t nx = st == (NST - 1) * C::STAGE ? 0 : st + C::STAGE;
+  auto step = [&](auto LOAD, int it, uint32_t st) {
+    const uint32_t nx = st == (NST - 1) * C::STAGE ? 0 : st + C::STAGE, before = st == 0 ? (NST - 1) * C::STAGE : st - C::STAGE;
     steps_of<0, PAIRS>([&](auto P) {
       constexpr int p = decltype(P)::value;
       constexpr bool last = p == PAIRS - 1;
@@ -263,11 +279,10 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
         tie(now[1]);
       }
       if constexpr (last) {
-        wait_vm<(NST - 2) * C::DMA>();
+        if constexpr (decltype(LOAD)::value) wait_vm<(NST - 2) * C::DMA>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        // every wave issues its loads over the pair's products
       }
       Operand a[2];
       steps_of<0, TN>([&](auto J) {
@@ -299,8 +314,11 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
         for (int i = 0; i < 2; ++i) sum[(p * TN + j) & 1][i] = block_sum(a[i], t);
         if constexpr (last) {
           read_tokens(J, nx);
-          constexpr int lo = C::DMA * j / TN, hi = C::DMA * (j + 1) / TN;
-          steps_of<lo, hi>([&](auto Q) { issue(Q, it + NST, st); });
+        }
+        if constexpr (decltype(LOAD)::value) {
+          constexpr int at = last ? j : TN + p * TN + j;       // group of the refill
+          constexpr int lo = at < SPAN ? C::DMA * at / SPAN : C::DMA, hi = at < SPAN ? C::DMA * (at + 1) / SPAN : C::DMA;
+          steps_of<lo, hi>([&](auto Q) { issue(Q, last ? it + NST : it + NST - 1, last ? st : before); });
         }
         __builtin_amdgcn_sched_barrier(0);
         scale_in(std::integral_constant<int, (p * TN + j + GROUPS - 1) % GROUPS>{});
@@ -311,8 +329,12 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
     return nx;
   };
   static_assert(PAIRS % 2 == 0, "pairs and groups alternate between two buffers: a step ends where the next expects it");
-  uint32_t st = 0;
-  for (int it = 0; it < steps.count; ++it) st = step(it, st);
+  auto loop = [&](auto LOAD) {
+    uint32_t st = 0;
+    for (int it = 0; it < steps.count; ++it) st = step(LOAD, it, st);
+  };
+  if (loader) loop(std::true_type{});
+  else loop(std::false_type{});
   scale_in(std::integral_constant<int, GROUPS - 1>{});
 
   wait_vm<0>();
@@ -334,6 +356,9 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   if (args.bias) load_row<8>(args.bias + m, left, bs);
 #pragma unroll
   for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(bs[i]));
+  // Rows of whole cache lines stream past the L2, which would only flush them (4096 x 2304 x 768 XXX us).
+  const __amdgpu_buffer_rsrc_t y_rsrc = uniform_rsrc(
+      (const OutT*)args.Y + (int64_t)(n0 + wn * C::WTN) * args.ldy + m0 + wm * C::WTM, 0xFFFFFFFFu);
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     const int n_first = n0 + wn * C::WTN + 16 * j;
@@ -373,6 +398,18 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = args.residual ? z[8 * t + i] + res[t][i] : z[8 * t + i];
+      if (args.stream && left >= 8) {
+        const uint32_t at = ((uint32_t)(16 * j + t * TPI + lane / LPT) * (uint32_t)args.ldy + 8 * (lane % LPT)) * sizeof(OutT);
+        if constexpr (EXACT) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            stream_16b(y_rsrc, (u32x4){__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                                       __float_as_uint(v[4 * h + 3])}, at + 16 * h);
+        } else {
+          stream_16b(y_rsrc, (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}, at);
+        }
+        continue;
+      }
       store_row<8>((OutT*)args.Y + (int64_t)n * args.ldy + m, left, v);
     }
   }
@@ -380,10 +417,10 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
 
 // (two waves a SIMD: with more registers the compiler would hand the block sums to the accumulation
 // registers, from where each goes back one by one)
-template <int BM, int BN, int WGM, int WGN, int NST, typename OutT>
+template <int BM, int BN, int WGM, int WGN, int LW, int NST, int SPAN, typename OutT>
 __global__ __launch_bounds__(WGM * WGN * 64, 2) void k_gemm_f8_block(const F8BArgs args) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * F8BTile<BM, BN, WGM, WGN, NST>::STAGE];
-  f8_block_scaled_tile<BM, BN, WGM, WGN, NST, OutT>(args, lds);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * F8BTile<BM, BN, WGM, WGN, LW, NST>::STAGE];
+  f8_block_scaled_tile<BM, BN, WGM, WGN, LW, NST, SPAN, OutT>(args, lds);
 }
 
 // Few tokens: a block has RT x 16 rows and TT x 16 tokens, and its W waves split K, wave w taking blocks of
@@ -499,12 +536,12 @@ static p24_status launch_block_tokens(const F8BArgs& a, hipStream_t st) {
   return launch_status();
 }
 
-template <int BM, int BN, int WGM, int WGN, int NST, typename OutT>
+template <int BM, int BN, int WGM, int WGN, int LW, int NST, int SPAN, typename OutT>
 static p24_status launch_block_tile(F8BArgs a, hipStream_t st) {
   a.nbm = (a.M + BM - 1) / BM;
   a.nbn = (a.N + BN - 1) / BN;
   if ((int64_t)a.nbm * a.nbn * (WGM * WGN * 64) > UINT32_MAX) return P24_ERR_UNSUPPORTED;   // a grid's threads
-  hipLaunchKernelGGL((k_gemm_f8_block<BM, BN, WGM, WGN, NST, OutT>), dim3((unsigned)(a.nbm * a.nbn)), dim3(WGM * WGN * 64), 0,
+  hipLaunchKernelGGL((k_gemm_f8_block<BM, BN, WGM, WGN, LW, NST, SPAN, OutT>), dim3((unsigned)(a.nbm * a.nbn)), dim3(WGM * WGN * 64), 0,
                      st, a);
   return launch_status();
 }
@@ -536,10 +573,10 @@ static p24_status launch_block(const F8BArgs& a, hipStream_t st) {
   constexpr bool EXACT = sizeof(OutT) == 4;
   switch (choose_block(a, EXACT)) {
     case F8BKernel::T256x256:
-      if constexpr (!EXACT) return launch_block_tile<256, 256, 2, 4, 2, OutT>(a, st);
-    case F8BKernel::T256x128: return launch_block_tile<256, 128, 4, 2, 3, OutT>(a, st);
-    case F8BKernel::T128x128: return launch_block_tile<128, 128, 2, 2, 2, OutT>(a, st);
-    case F8BKernel::T64x64: return launch_block_tile<64, 64, 1, 4, 3, OutT>(a, st);
+      if constexpr (!EXACT) return launch_block_tile<256, 256, 2, 4, 8, 2, 12, OutT>(a, st);
+    case F8BKernel::T256x128: return launch_block_tile<256, 128, 4, 2, 8, 3, 8, OutT>(a, st);
+    case F8BKernel::T128x128: return launch_block_tile<128, 128, 2, 2, 4, 2, 4, OutT>(a, st);
+    case F8BKernel::T64x64: return launch_block_tile<64, 64, 1, 4, 4, 3, 1, OutT>(a, st);
     case F8BKernel::TOKENS: break;
   }
   if (a.N <= 16) return launch_block_tokens<8, 1, 1, OutT>(a, st);
@@ -587,6 +624,7 @@ extern "C" P24_API p24_status gemm_f8_block(const void* W, int64_t ldw, const fl
   a.N = (int)N;
   a.K = (int)K;
   a.act = act;
+  a.stream = aligned(Y, 128) && ldy * (int64_t)ye % 128 == 0 && (uint64_t)ldy * 2048 < (1ull << 32);
   if (y_dtype == P24_F32) return launch_block<float>(a, (hipStream_t)stream);
   return launch_block<uint16_t>(a, (hipStream_t)stream);
 }
