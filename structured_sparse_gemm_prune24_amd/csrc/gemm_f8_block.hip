@@ -119,16 +119,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* p, ui
   return f8_rsrc((const uint8_t*)(uintptr_t)((uint64_t)hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
 }
 
-template <int BM, int BN, int WGM, int WGN, int LW, int NST, int SPAN, typename OutT>
-__device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_t* lds) {
-  using C = F8BTile<BM, BN, WGM, WGN, LW, NST>;
+template <int BM, int BN, int WGM, int WGN, int LW, int NST, int KG, int SPAN, typename OutT>
+__device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_t* lds_all) {
+  using C = F8BTile<BM, BN, WGM, WGN, LW, NST, KG>;
   constexpr bool EXACT = sizeof(OutT) == 4;
   constexpr int TM = C::TM, TN = C::TN, PAIRS = C::PAIRS;
   typedef F8BOperand<EXACT> Operand;
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = KG == 1 ? 0 : wave_id / C::WAVES, wave = KG == 1 ? wave_id : wave_id % C::WAVES;
   const int wm = wave / WGN, wn = wave % WGN;
+  uint8_t* lds = lds_all + kg * (NST * C::STAGE);       // this group's stages
 
   // block -> tile: each XCD a contiguous range, in groups of eight row blocks
   const uint32_t b = xcd_remap(blockIdx.x, (uint32_t)args.nbm * args.nbn);
@@ -141,6 +143,8 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   const int m_rows = min(args.M - m0, BM), n_rows = min(args.N - n0, BN);
 
   const F8BSteps steps(args.K);
+  // this group's steps; the groups' counts differ by one at most
+  const int k_first = (int)((int64_t)steps.count * kg / KG), count = (int)((int64_t)steps.count * (kg + 1) / KG) - k_first;
   const F8BReads<LW> x_reads(lane, wave, args.ldx, steps), w_reads(lane, wave, args.ldw, steps);
   const __amdgpu_buffer_rsrc_t x_rsrc =
       uniform_rsrc(args.X + (int64_t)n0 * args.ldx, F8BReads<LW>::bytes(n_rows, args.ldx, args.K));
@@ -157,11 +161,11 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
     s_voff[q] = F8BScaleReads<C>::vector(lane, F8BScaleReads<C>::number(wave, q), n_rows, row_blocks, steps.count);
   const bool loader = LW == C::WAVES || wave < LW;
 
-  // load Q of this wave for step `it` into the stage at byte st
+  // load Q of this wave for its group's step `it` (its last one past the end) into the stage at byte st
   auto issue = [&](auto Q, int it, uint32_t st) {
     constexpr int q = decltype(Q)::value;
-    const int block = steps.block(it);
-    const bool part = last_of(it, steps.count) == 0;
+    const int s_all = k_first + last_of(it, count), block = steps.block(s_all);
+    const bool part = s_all == 0;
     if constexpr (q < C::X_DMA) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(x_rsrc, (lds_void_b*)(lds + st + (q * LW + wave) * 1024), 16,
                                                x_reads.vector(q, part), F8BReads<LW>::scalar(block), 0, 0);
@@ -250,10 +254,10 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   asm volatile("" ::: "memory");
   if (steps.rest) {
     // the first step's weights past K, whose tokens repeat chunk 0: zeros
-    for (int u = threadIdx.x; u < BM * 8; u += C::WAVES * 64) {
+    for (int u = threadIdx.x; u < BM * 8; u += C::WAVES * KG * 64) {
       const int n = u >> 3, c = u & 7;
       if (16 * c >= steps.rest)
-        *reinterpret_cast<u32x4*>(lds + C::X_BYTES + (n ^ ((n >> 3) & 1)) * 128 + ((c ^ (n & 7)) * 16)) = (u32x4){0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(lds_all + C::X_BYTES + (n ^ ((n >> 3) & 1)) * 128 + ((c ^ (n & 7)) * 16)) = (u32x4){0, 0, 0, 0};
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -331,7 +335,8 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   static_assert(PAIRS % 2 == 0, "pairs and groups alternate between two buffers: a step ends where the next expects it");
   auto loop = [&](auto LOAD) {
     uint32_t st = 0;
-    for (int it = 0; it < steps.count; ++it) st = step(LOAD, it, st);
+    for (int it = 0; it < count; ++it) st = step(LOAD, it, st);
+    if (KG > 1 && count * KG < steps.count) __builtin_amdgcn_s_barrier();      // the other groups' last step
   };
   if (loader) loop(std::true_type{});
   else loop(std::false_type{});
@@ -346,9 +351,13 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   asm volatile("" ::: "memory");
 
   // Epilogue by slices of 16 tokens through LDS as fp32, so that a lane holds eight consecutive
-  // features of a token for bias, activation, residual and store, the same features for every token.
-  constexpr int LPT = C::WTM / 8, TPI = 64 / LPT, PASSES = 16 / TPI;      // lanes per token, tokens per pass, passes
-  float* part = reinterpret_cast<float*>(lds) + wave * 16 * C::PITCH;
+  // features of a token for bias, activation, residual and store, the same features for every token.  With split K the
+  // groups' parts meet here, summed in group order, and the groups share the slice's passes.
+  constexpr int LPT = C::WTM / 8, TPI = 64 / LPT;      // lanes per token, tokens per pass
+  constexpr int PASSES = 16 / TPI / KG;                // a group's passes
+  static_assert(PASSES * KG * TPI == 16, "the groups share the passes evenly");
+  constexpr int PARTS = C::WAVES * 16 * C::PITCH;      // floats of one group's slices
+  float* part = reinterpret_cast<float*>(lds_all) + wave * 16 * C::PITCH;
   const int m = m0 + wm * C::WTM + 8 * (lane % LPT), left = args.M - m;
   float bs[8];
 #pragma unroll
@@ -356,17 +365,19 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   if (args.bias) load_row<8>(args.bias + m, left, bs);
 #pragma unroll
   for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(bs[i]));
-  // Rows of whole cache lines stream past the L2, which would only flush them (4096 x 2304 x 768 XXX us).
+  // Rows of whole cache lines stream past the L2, which would only flush them (4096 x 2304 x 768 18.2 -> 16.1 us).
   const __amdgpu_buffer_rsrc_t y_rsrc = uniform_rsrc(
       (const OutT*)args.Y + (int64_t)(n0 + wn * C::WTN) * args.ldy + m0 + wm * C::WTM, 0xFFFFFFFFu);
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
-    const int n_first = n0 + wn * C::WTN + 16 * j;
+    // token of pass t, within the wave's
+    auto token = [&](int t) { return 16 * j + (kg * PASSES + t) * TPI + lane / LPT; };
+    const int n_wave = n0 + wn * C::WTN;
     float z[8 * PASSES], res[PASSES][8];
     if (args.residual) {
 #pragma unroll
       for (int t = 0; t < PASSES; ++t) {
-        const int n = n_first + t * TPI + lane / LPT;
+        const int n = n_wave + token(t);
         if constexpr (EXACT) {
           float lo[4], hi[4];
           load_row<4>((const float*)args.residual + (int64_t)n * args.ldr + m, n < args.N ? left : 0, lo);
@@ -381,25 +392,32 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
         }
       }
     }
+    if (KG > 1 && j > 0) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TM; ++i) *reinterpret_cast<f32x4*>(part + r * C::PITCH + 16 * i + 4 * c0) = acc[i][j];
+    for (int i = 0; i < TM; ++i)
+      *reinterpret_cast<f32x4*>(part + kg * PARTS + r * C::PITCH + 16 * i + 4 * c0) = acc[i][j];
+    if (KG > 1) __syncthreads();
 #pragma unroll
     for (int t = 0; t < PASSES; ++t) {
-      const float* row = part + (t * TPI + lane / LPT) * C::PITCH + 8 * (lane % LPT);
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(row), hi = *reinterpret_cast<const f32x4*>(row + 4);
+      const float* row = part + (token(t) - 16 * j) * C::PITCH + 8 * (lane % LPT);
+      f32x4 lo = *reinterpret_cast<const f32x4*>(row), hi = *reinterpret_cast<const f32x4*>(row + 4);
+#pragma unroll
+      for (int g = 1; g < KG; ++g) {
+        lo += *reinterpret_cast<const f32x4*>(row + g * PARTS);
+        hi += *reinterpret_cast<const f32x4*>(row + g * PARTS + 4);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[8 * t + i] = (i < 4 ? lo[i] : hi[i - 4]) + bs[i];
     }
     f8_act<EXACT>(z, args.act);
 #pragma unroll
     for (int t = 0; t < PASSES; ++t) {
-      const int n = n_first + t * TPI + lane / LPT;
-      if (n >= args.N) continue;
+      if (n_wave + token(t) >= args.N) continue;
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = args.residual ? z[8 * t + i] + res[t][i] : z[8 * t + i];
       if (args.stream && left >= 8) {
-        const uint32_t at = ((uint32_t)(16 * j + t * TPI + lane / LPT) * (uint32_t)args.ldy + 8 * (lane % LPT)) * sizeof(OutT);
+        const uint32_t at = ((uint32_t)token(t) * (uint32_t)args.ldy + 8 * (lane % LPT)) * sizeof(OutT);
         if constexpr (EXACT) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -408,19 +426,19 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
         } else {
           stream_16b(y_rsrc, (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}, at);
         }
-        continue;
+      } else {
+        store_row<8>((OutT*)args.Y + (int64_t)(n_wave + token(t)) * args.ldy + m, left, v);
       }
-      store_row<8>((OutT*)args.Y + (int64_t)n * args.ldy + m, left, v);
     }
   }
 }
 
 // (two waves a SIMD: with more registers the compiler would hand the block sums to the accumulation
 // registers, from where each goes back one by one)
-template <int BM, int BN, int WGM, int WGN, int LW, int NST, int SPAN, typename OutT>
-__global__ __launch_bounds__(WGM * WGN * 64, 2) void k_gemm_f8_block(const F8BArgs args) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * F8BTile<BM, BN, WGM, WGN, LW, NST>::STAGE];
-  f8_block_scaled_tile<BM, BN, WGM, WGN, LW, NST, SPAN, OutT>(args, lds);
+template <int BM, int BN, int WGM, int WGN, int LW, int NST, int KG, int SPAN, typename OutT>
+__global__ __launch_bounds__(WGM * WGN * KG * 64, 2) void k_gemm_f8_block(const F8BArgs args) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NST * F8BTile<BM, BN, WGM, WGN, LW, NST, KG>::STAGE];
+  f8_block_scaled_tile<BM, BN, WGM, WGN, LW, NST, KG, SPAN, OutT>(args, lds);
 }
 
 // Few tokens: a block has RT x 16 rows and TT x 16 tokens, and its W waves split K, wave w taking blocks of
@@ -536,17 +554,18 @@ static p24_status launch_block_tokens(const F8BArgs& a, hipStream_t st) {
   return launch_status();
 }
 
-template <int BM, int BN, int WGM, int WGN, int LW, int NST, int SPAN, typename OutT>
+template <int BM, int BN, int WGM, int WGN, int LW, int NST, int KG, int SPAN, typename OutT>
 static p24_status launch_block_tile(F8BArgs a, hipStream_t st) {
   a.nbm = (a.M + BM - 1) / BM;
   a.nbn = (a.N + BN - 1) / BN;
-  if ((int64_t)a.nbm * a.nbn * (WGM * WGN * 64) > UINT32_MAX) return P24_ERR_UNSUPPORTED;   // a grid's threads
-  hipLaunchKernelGGL((k_gemm_f8_block<BM, BN, WGM, WGN, LW, NST, SPAN, OutT>), dim3((unsigned)(a.nbm * a.nbn)), dim3(WGM * WGN * 64), 0,
-                     st, a);
+  constexpr int THREADS = WGM * WGN * KG * 64;
+  if ((int64_t)a.nbm * a.nbn * THREADS > UINT32_MAX) return P24_ERR_UNSUPPORTED;   // a grid's threads
+  hipLaunchKernelGGL((k_gemm_f8_block<BM, BN, WGM, WGN, LW, NST, KG, SPAN, OutT>), dim3((unsigned)(a.nbm * a.nbn)),
+                     dim3(THREADS), 0, st, a);
   return launch_status();
 }
 
-enum class F8BKernel { TOKENS, T64x64, T128x128, T256x128, T256x256 };
+enum class F8BKernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x256 };
 
 static int64_t block_tiles(const F8BArgs& a, int bm, int bn) {
   return ((a.M + (int64_t)bm - 1) / bm) * ((a.N + (int64_t)bn - 1) / bn);
@@ -556,7 +575,9 @@ static F8BKernel choose_block(const F8BArgs& a, bool exact) {
   if (const char* e = getenv("P24_F8_TILE")) {
     auto is = [&](const char* name) { return strcmp(e, name) == 0; };
     if (is("tokens")) return F8BKernel::TOKENS;
+    if (is("64x32")) return F8BKernel::T64x32;
     if (is("64x64")) return F8BKernel::T64x64;
+    if (is("128x64")) return F8BKernel::T128x64;
     if (is("128x128")) return F8BKernel::T128x128;
     if (is("256x128") || (exact && is("256x256"))) return F8BKernel::T256x128;
     if (is("256x256")) return F8BKernel::T256x256;
@@ -571,12 +592,22 @@ static F8BKernel choose_block(const F8BArgs& a, bool exact) {
 template <typename OutT>
 static p24_status launch_block(const F8BArgs& a, hipStream_t st) {
   constexpr bool EXACT = sizeof(OutT) == 4;
+  // one round of blocks: groups of waves split K inside a block
+  auto split = [&](int bm, int bn) { return a.K >= 1024 && block_tiles(a, bm, bn) <= 256; };
   switch (choose_block(a, EXACT)) {
     case F8BKernel::T256x256:
-      if constexpr (!EXACT) return launch_block_tile<256, 256, 2, 4, 8, 2, 12, OutT>(a, st);
-    case F8BKernel::T256x128: return launch_block_tile<256, 128, 4, 2, 8, 3, 8, OutT>(a, st);
-    case F8BKernel::T128x128: return launch_block_tile<128, 128, 2, 2, 4, 2, 4, OutT>(a, st);
-    case F8BKernel::T64x64: return launch_block_tile<64, 64, 1, 4, 4, 3, 1, OutT>(a, st);
+      if constexpr (!EXACT) return launch_block_tile<256, 256, 2, 4, 8, 2, 1, 12, OutT>(a, st);
+    case F8BKernel::T256x128: return launch_block_tile<256, 128, 4, 2, 8, 3, 1, 8, OutT>(a, st);
+    case F8BKernel::T128x128: return launch_block_tile<128, 128, 2, 2, 4, 2, 1, 8, OutT>(a, st);
+    case F8BKernel::T128x64:
+      if (split(128, 64)) return launch_block_tile<128, 64, 2, 2, 4, 3, 2, 4, OutT>(a, st);
+      return launch_block_tile<128, 64, 2, 2, 4, 3, 1, 4, OutT>(a, st);
+    case F8BKernel::T64x64:
+      if (split(64, 64)) return launch_block_tile<64, 64, 1, 4, 4, 4, 2, 2, OutT>(a, st);
+      return launch_block_tile<64, 64, 1, 4, 4, 3, 1, 2, OutT>(a, st);
+    case F8BKernel::T64x32:
+      if (split(64, 32)) return launch_block_tile<64, 32, 1, 2, 2, 3, 2, 2, OutT>(a, st);
+      return launch_block_tile<64, 32, 1, 2, 2, 3, 1, 2, OutT>(a, st);
     case F8BKernel::TOKENS: break;
   }
   if (a.N <= 16) return launch_block_tokens<8, 1, 1, OutT>(a, st);

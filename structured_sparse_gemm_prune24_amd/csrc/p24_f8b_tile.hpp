@@ -7,10 +7,11 @@
 namespace p24 {
 
 // BM rows x BN tokens per block on WGM x WGN waves, of which the first LW load; K by 128 values (one block of
-// scales) a step, NST steps in LDS.
-template <int BM, int BN, int WGM, int WGN, int LW_, int NST>
+// scales) a step, NST steps in LDS.  With KG > 1 there are KG such groups of waves, each with its own stages and
+// its own part of K.
+template <int BM, int BN, int WGM, int WGN, int LW_, int NST, int KG>
 struct F8BTile {
-  static constexpr int WAVES = WGM * WGN, LW = LW_;
+  static constexpr int WAVES = WGM * WGN, LW = LW_;        // of a group
   static constexpr int WTM = BM / WGM, WTN = BN / WGN;     // wave tile
   static constexpr int TM = WTM / 16, TN = WTN / 16;       // its 16 x 16 tiles
   static constexpr int PAIRS = TM / 2;                     // rows go by 32
@@ -28,7 +29,7 @@ struct F8BTile {
   static_assert(LW % 2 == 0 && LW <= WAVES && BN % (8 * LW) == 0 && BM % (8 * LW) == 0, "even loads");
   static_assert(PAIRS >= 2 && TM % 2 == 0 && TN >= 1, "rows go by pairs of tiles, two pairs at least");
   static_assert(WTM <= 128 && 128 % WTM == 0, "a wave's rows lie in one block of scales");
-  static_assert(NST * STAGE <= 160 * 1024 && WAVES * 16 * PITCH * 4 <= NST * STAGE, "LDS");
+  static_assert(KG * NST * STAGE <= 160 * 1024 && WAVES * 16 * PITCH * 4 <= NST * STAGE, "LDS");
   static_assert(NST * DMA < 64, "vmcnt range");
 };
 

@@ -176,12 +176,12 @@ def test_product(N, M, K, out):
     _check_product(w, x, r=r, out=out)
 
 
-TILES = ["tokens", "64x64", "128x128", "256x128", "256x256"]
+TILES = ["tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x256"]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("N,M,K", [(1, 1, 16), (33, 65, 128), (70, 300, 192), (129, 257, 400), (257, 260, 1024),
-                                   (100, 129, 1088), (300, 513, 1472), (64, 128, 4176), (300, 520, 64), (260, 264, 256), (513, 512, 512)])
+                                   (100, 129, 1088), (300, 513, 1472), (64, 128, 4176), (70, 129, 1168), (300, 520, 64), (260, 264, 256), (513, 512, 512)])
 @pytest.mark.parametrize("tile", TILES)
 def test_product_of_every_kernel(monkeypatch, tile, N, M, K, out):
     """Each kernel off its tile in tokens, rows and K, on wider buffers; rows that the tile reaches past the output stay
