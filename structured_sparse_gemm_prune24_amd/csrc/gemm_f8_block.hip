@@ -17,6 +17,7 @@
 #include "../../include/prune24_f8_block.h"
 #include "p24_api_internal.hpp"
 #include "p24_f8.hpp"
+#include "p24_f8_cost.hpp"
 #include "p24_f8b_tile.hpp"
 
 namespace p24 {
@@ -187,7 +188,7 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
 
   // LDS read addresses in stage 0: chunks 2 (L / 16) and one on of row L % 16 of a 16-row tile.  Sixteen lanes read
   // at a time, half of them of the next lane group: with chunk L / 16 there they met on the same banks
-  // (8192^3 475 -> XXX us).
+  // (8192^3 475 -> 450 us with the sums' delay below).
   const uint32_t base = (uint32_t)(uintptr_t)(lds_void_b*)lds;
   const int r = lane & 15, c0 = lane >> 4;
   const uint32_t in_tile = (uint32_t)((r ^ (r >> 3)) * 128);
@@ -565,7 +566,26 @@ static p24_status launch_block_tile(F8BArgs a, hipStream_t st) {
   return launch_status();
 }
 
-enum class F8BKernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x256 };
+// Which kernel: that of the fewest microseconds (p24_f8_cost.hpp).  Over 120 shapes drawn at random the choice is 2 %
+// behind the fastest, for both outputs (geometric mean).  Measured, us, M x K with N tokens (bf16; fp32):
+//   8192 x 8192, 8192    256x256 435, 256x128 500, 128x128 541; 128x128 889
+//   8192 x 4096, 4096    256x256 117, 256x128 133, 128x128 146; 128x128 240, 128x64 287
+//   4096 x 11264, 2048   256x128 86, 128x128 94, 256x256 125
+//   4096 x 4096, 512     128x64 15.7, 64x64 16.5, 64x32 19.0
+//   1000 x 4048, 517     64x64 11.6, 64x32 14.0; 64x64 17.3, 128x64 22.7
+//   4096 x 4096, 32      tokens 8.6, 64x32 9.1;  1 token 5.1, 8.9
+enum F8BKernel { B_TOKENS, B_64x32, B_64x64, B_128x64, B_128x128, B_256x128, B_256x256, B_KERNELS };
+
+constexpr TileCost BLOCK_BF16[B_KERNELS] = {
+    {16, 32, 3.45, 0.053, 1.07, 0.108},  {64, 32, 4.19, 0.195, 0.75, 0.189},   {64, 64, 4.21, 0.251, 1.14, 0.276},
+    {128, 64, 4.84, 0.330, 2.04, 0.413}, {128, 128, 5.45, 0.620, 2.74, 0.621}, {256, 128, 6.18, 0.690, 6.77, 1.01},
+    {256, 256, 7.78, 1.19, 9.83, 1.70},
+};
+// (with the conversions of an fp32 output taller tiles are no faster)
+constexpr TileCost BLOCK_F32[B_256x128] = {
+    {16, 32, 3.52, 0.060, 1.27, 0.111},  {64, 32, 4.73, 0.292, 0.93, 0.224},   {64, 64, 4.43, 0.438, 1.51, 0.353},
+    {128, 64, 5.40, 0.554, 2.71, 0.544}, {128, 128, 6.06, 1.02, 4.36, 0.872},
+};
 
 static int64_t block_tiles(const F8BArgs& a, int bm, int bn) {
   return ((a.M + (int64_t)bm - 1) / bm) * ((a.N + (int64_t)bn - 1) / bn);
@@ -573,42 +593,44 @@ static int64_t block_tiles(const F8BArgs& a, int bm, int bn) {
 
 static F8BKernel choose_block(const F8BArgs& a, bool exact) {
   if (const char* e = getenv("P24_F8_TILE")) {
-    auto is = [&](const char* name) { return strcmp(e, name) == 0; };
-    if (is("tokens")) return F8BKernel::TOKENS;
-    if (is("64x32")) return F8BKernel::T64x32;
-    if (is("64x64")) return F8BKernel::T64x64;
-    if (is("128x64")) return F8BKernel::T128x64;
-    if (is("128x128")) return F8BKernel::T128x128;
-    if (is("256x128") || (exact && is("256x256"))) return F8BKernel::T256x128;
-    if (is("256x256")) return F8BKernel::T256x256;
+    static const char* const names[B_KERNELS] = {"tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x256"};
+    for (int i = 0; i < B_KERNELS; ++i)
+      if (strcmp(e, names[i]) == 0) return exact && i > B_128x128 ? B_128x128 : (F8BKernel)i;
   }
-  if (a.N <= 32) return F8BKernel::TOKENS;
-  if (!exact && block_tiles(a, 256, 256) >= 144) return F8BKernel::T256x256;
-  if (block_tiles(a, 256, 128) >= 144) return F8BKernel::T256x128;
-  if (block_tiles(a, 128, 128) >= 144) return F8BKernel::T128x128;
-  return F8BKernel::T64x64;
+  const TileCost* costs = exact ? BLOCK_F32 : BLOCK_BF16;
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < (exact ? B_256x128 : B_KERNELS); ++i) {
+    const double us = costs[i].us((double)block_tiles(a, costs[i].bm, costs[i].bn), a.K);
+    if (i == 0 || us < least) {
+      least = us;
+      best = i;
+    }
+  }
+  return (F8BKernel)best;
 }
 
 template <typename OutT>
 static p24_status launch_block(const F8BArgs& a, hipStream_t st) {
   constexpr bool EXACT = sizeof(OutT) == 4;
   // one round of blocks: groups of waves split K inside a block
-  auto split = [&](int bm, int bn) { return a.K >= 1024 && block_tiles(a, bm, bn) <= 256; };
+  auto split = [&](int bm, int bn, int round) { return a.K >= 1024 && block_tiles(a, bm, bn) <= round; };
   switch (choose_block(a, EXACT)) {
-    case F8BKernel::T256x256:
+    case B_256x256:
       if constexpr (!EXACT) return launch_block_tile<256, 256, 2, 4, 8, 2, 1, 12, OutT>(a, st);
-    case F8BKernel::T256x128: return launch_block_tile<256, 128, 4, 2, 8, 3, 1, 8, OutT>(a, st);
-    case F8BKernel::T128x128: return launch_block_tile<128, 128, 2, 2, 4, 2, 1, 8, OutT>(a, st);
-    case F8BKernel::T128x64:
-      if (split(128, 64)) return launch_block_tile<128, 64, 2, 2, 4, 3, 2, 4, OutT>(a, st);
+    case B_256x128:
+      if constexpr (!EXACT) return launch_block_tile<256, 128, 4, 2, 8, 3, 1, 8, OutT>(a, st);
+    case B_128x128: return launch_block_tile<128, 128, 2, 2, 4, 2, 1, 8, OutT>(a, st);
+    case B_128x64:
+      if (split(128, 64, 256)) return launch_block_tile<128, 64, 2, 2, 4, 3, 2, 4, OutT>(a, st);
       return launch_block_tile<128, 64, 2, 2, 4, 3, 1, 4, OutT>(a, st);
-    case F8BKernel::T64x64:
-      if (split(64, 64)) return launch_block_tile<64, 64, 1, 4, 4, 4, 2, 2, OutT>(a, st);
+    case B_64x64:
+      if (split(64, 64, 256)) return launch_block_tile<64, 64, 1, 4, 4, 4, 2, 2, OutT>(a, st);
       return launch_block_tile<64, 64, 1, 4, 4, 3, 1, 2, OutT>(a, st);
-    case F8BKernel::T64x32:
-      if (split(64, 32)) return launch_block_tile<64, 32, 1, 2, 2, 3, 2, 2, OutT>(a, st);
+    case B_64x32:
+      if (split(64, 32, 512)) return launch_block_tile<64, 32, 1, 2, 2, 3, 2, 2, OutT>(a, st);
       return launch_block_tile<64, 32, 1, 2, 2, 3, 1, 2, OutT>(a, st);
-    case F8BKernel::TOKENS: break;
+    default: break;
   }
   if (a.N <= 16) return launch_block_tokens<8, 1, 1, OutT>(a, st);
   return launch_block_tokens<8, 1, 2, OutT>(a, st);

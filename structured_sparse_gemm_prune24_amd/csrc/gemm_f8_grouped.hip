@@ -11,6 +11,7 @@
 
 #include "../../include/prune24_experts.h"
 #include "p24_api_internal.hpp"
+#include "p24_f8_cost.hpp"
 #include "p24_f8_gemm.hpp"
 
 namespace p24 {
@@ -105,77 +106,63 @@ static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
 
 // Which kernel.  Where the rows lie is not known here: the experts' numbers of rows are taken as
 // exponentially distributed, so that an expert with a rows on average has 1 / (1 - exp(-BN / a)) tiles of BN rows.
-// A block tile takes a time that was measured with all CUs at work, us: `tile` once (first loads,
-// epilogue) and `step` for each 128 of K; the blocks come in rounds of 256.  The fewest microseconds win.
-// That ranks the kernels and is no forecast: decoding sizes are bound by the weights' bytes.
+// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp): over 70 shapes drawn at
+// random it is 1.6 % behind the fastest of the eight for bf16 outputs, 1.3 % for fp32 (geometric mean).
 // Measured, us (T tokens of k experts, of E with M x K):
 //   4096 of 8, 64 of 4096 x 2048   256x256 234, 256x192 249, 256x128 269, 128x128 320, 64x64 496
 //   1024 of 8, 64 of 4096 x 2048   256x192 102, 256x128 106, 128x128 117, 256x256 120
 //   256 of 8, 128 of 2048 x 2048   128x64 65, 256x128 68, 64x32 72, tokens 116
 //   64 of 4, 32 of 4096 x 4096     64x32 59, 128x64 59, 64x64 64, tokens 73
-// The kernel without shared operands starts sooner but reads each row once per 32 features:
 //   1 of 8, 128 of 2048 x 4096     tokens 9.1, 64x32 13.6
-//   8 of 8, 64 of 2048 x 2048      tokens 25.7, 64x32 22.2
-// Over 70 shapes drawn at random (both outputs) the choice is 4 % behind the fastest of the eight (geometric mean).
-enum class F8GroupedKernel { TOKENS, T64x32, T64x64, T128x64, T128x128, T256x128, T256x192, T256x256 };
+enum F8GroupedKernel { G_TOKENS, G_64x32, G_64x64, G_128x64, G_128x128, G_256x128, G_256x192, G_256x256, G_KERNELS };
 
-struct F8GroupedCost {
-  F8GroupedKernel kernel;
-  int bm, bn;
-  double tile, step;
+constexpr TileCost GROUPED_BF16[G_KERNELS] = {
+    {32, 32, 3.96, 0.064, 0.42, 0.139},  {64, 32, 5.50, 0.250, 0.85, 0.149},   {64, 64, 5.65, 0.255, 1.10, 0.180},
+    {128, 64, 5.56, 0.257, 1.95, 0.327}, {128, 128, 6.20, 0.319, 3.01, 0.378}, {256, 128, 7.05, 0.407, 5.78, 0.797},
+    {256, 192, 8.12, 0.502, 6.14, 1.08}, {256, 256, 9.03, 0.681, 8.10, 1.08},
 };
-constexpr F8GroupedCost GROUPED_COSTS[] = {
-    {F8GroupedKernel::T64x32, 64, 32, 1.27, 0.074},     {F8GroupedKernel::T64x64, 64, 64, 1.63, 0.126},
-    {F8GroupedKernel::T128x64, 128, 64, 3.26, 0.157},   {F8GroupedKernel::T128x128, 128, 128, 4.7, 0.263},
-    {F8GroupedKernel::T256x128, 256, 128, 6.5, 0.525},  {F8GroupedKernel::T256x192, 256, 192, 8.7, 0.65},
-    {F8GroupedKernel::T256x256, 256, 256, 8.8, 0.91},
+// (the widened operands of an fp32 output do not fit the registers of the two widest)
+constexpr TileCost GROUPED_F32[G_256x192] = {
+    {32, 32, 4.17, 0.074, 0.45, 0.151},  {64, 32, 5.37, 0.480, 1.00, 0.178},   {64, 64, 5.60, 0.461, 1.38, 0.237},
+    {128, 64, 5.75, 0.463, 2.67, 0.385}, {128, 128, 6.58, 0.541, 3.97, 0.575}, {256, 128, 7.36, 0.869, 8.26, 1.07},
 };
 
 static F8GroupedKernel choose_grouped(const F8GroupedArgs& g, bool exact) {
   if (const char* e = getenv("P24_F8_TILE")) {
-    auto is = [&](const char* name) { return strcmp(e, name) == 0; };
-    if (is("tokens")) return F8GroupedKernel::TOKENS;
-    if (is("64x32")) return F8GroupedKernel::T64x32;
-    if (is("64x64")) return F8GroupedKernel::T64x64;
-    if (is("128x64")) return F8GroupedKernel::T128x64;
-    if (is("128x128")) return F8GroupedKernel::T128x128;
-    if (is("256x128") || (exact && (is("256x192") || is("256x256")))) return F8GroupedKernel::T256x128;
-    if (is("256x192")) return F8GroupedKernel::T256x192;
-    if (is("256x256")) return F8GroupedKernel::T256x256;
+    static const char* const names[G_KERNELS] = {"tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x192", "256x256"};
+    for (int i = 0; i < G_KERNELS; ++i)
+      if (strcmp(e, names[i]) == 0) return exact && i > G_256x128 ? G_256x128 : (F8GroupedKernel)i;
   }
+  const TileCost* costs = exact ? GROUPED_F32 : GROUPED_BF16;
   const double rows = g.groups.rows, experts = g.groups.experts;
   const double live = experts * -expm1(-rows / experts), mean = rows / live;    // experts with rows, theirs on average
-  auto blocks = [&](int bm, int bn) { return live / -expm1(-bn / mean) * ((g.a.M + bm - 1) / bm); };
-  const double small = blocks(32, 32);
-  if (small <= 800 || (small <= 1500 && g.a.K <= 1408)) return F8GroupedKernel::TOKENS;
-  F8GroupedKernel best = F8GroupedKernel::T64x32;
-  double least = 1e300;
-  for (const F8GroupedCost& c : GROUPED_COSTS) {
-    if (exact && c.bn > 128) continue;    // widened operands do not fit their registers
-    const double b = blocks(c.bm, c.bn), rounds = b < 256 ? 1.0 : b / 256;
-    const double us = rounds * (c.tile + c.step * ((g.a.K + 127) / 128));
-    if (us < least) {
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < (exact ? G_256x192 : G_KERNELS); ++i) {
+    const TileCost& c = costs[i];
+    const double us = c.us(live / -expm1(-c.bn / mean) * ((g.a.M + c.bm - 1) / c.bm), g.a.K);
+    if (i == 0 || us < least) {
       least = us;
-      best = c.kernel;
+      best = i;
     }
   }
-  return best;
+  return (F8GroupedKernel)best;
 }
 
 template <typename OutT>
 static p24_status launch_grouped(const F8GroupedArgs& g, hipStream_t st) {
   constexpr bool EXACT = sizeof(OutT) == 4;
   switch (choose_grouped(g, EXACT)) {
-    case F8GroupedKernel::T256x256:
+    case G_256x256:
       if constexpr (!EXACT) return launch_tile_grouped<256, 256, 2, 4, 8, 1, OutT>(g, st);
-    case F8GroupedKernel::T256x192:
+    case G_256x192:
       if constexpr (!EXACT) return launch_tile_grouped<256, 192, 4, 2, 4, 1, OutT>(g, st);
-    case F8GroupedKernel::T256x128: return launch_tile_grouped<256, 128, 4, 2, 4, 1, OutT>(g, st);
-    case F8GroupedKernel::T128x128: return launch_tile_grouped<128, 128, 2, 4, 4, 1, OutT>(g, st);
-    case F8GroupedKernel::T128x64: return launch_tile_grouped<128, 64, 2, 2, 4, 1, OutT>(g, st);
-    case F8GroupedKernel::T64x64: return launch_tile_grouped<64, 64, 2, 2, 4, 1, OutT>(g, st);
-    case F8GroupedKernel::T64x32: return launch_tile_grouped<64, 32, 2, 1, 2, 1, OutT>(g, st);
-    case F8GroupedKernel::TOKENS: break;
+    case G_256x128: return launch_tile_grouped<256, 128, 4, 2, 4, 1, OutT>(g, st);
+    case G_128x128: return launch_tile_grouped<128, 128, 2, 4, 4, 1, OutT>(g, st);
+    case G_128x64: return launch_tile_grouped<128, 64, 2, 2, 4, 1, OutT>(g, st);
+    case G_64x64: return launch_tile_grouped<64, 64, 2, 2, 4, 1, OutT>(g, st);
+    case G_64x32: return launch_tile_grouped<64, 32, 2, 1, 2, 1, OutT>(g, st);
+    default: break;
   }
   if (g.a.K >= 2048 && ((int64_t)g.a.M + 31) / 32 * f8_most_tiles(g, 32) <= 256) return launch_tokens_grouped<16, OutT>(g, st);
   if (g.a.K >= 1024) return launch_tokens_grouped<8, OutT>(g, st);
