@@ -45,19 +45,23 @@ enum { P24_SCORE_SOFTMAX = 0, P24_SCORE_SIGMOID = 1 };
  *             Computed in fp32.  A NaN logit, or +inf under softmax, gives the NaN
  *             that the formula gives.
  *   experts   T x k int32: the chosen experts, best first; -1 past the open ones.
- *             16 B aligned.
  *   weights   T x k fp32; 0 where there is no expert.
  *   offsets   E + 1 int32: expert e's rows are [offsets[e], offsets[e + 1]).
  *   tokens    T k int32: the token of each row; -1 from offsets[E] on.
  *   positions T x k int32: the row of a token's slot; -1 where there is no expert.
+ *   ws        experts_route_workspace(T, E) bytes (0 up to 64 tokens), 4 B aligned;
+ *             its contents need no preparation and mean nothing afterwards.  Calls
+ *             that may overlap need one each.
  *   1 <= k <= min(E, P24_EXPERTS_K_MAX), E <= P24_EXPERTS_MAX, T <= 2^18 (else
  *   P24_ERR_UNSUPPORTED).  T == 0 sets offsets to 0.  The outputs overlap no input
  *   and not each other.
  */
+P24_API size_t experts_route_workspace(int64_t T, int64_t E);
 P24_API p24_status experts_route(const void* logits, int32_t l_dtype, int64_t ldl, int64_t T, int64_t E,
                                  int64_t k, int32_t score, const float* bias, int32_t normalize,
                                  float scale, int32_t* experts, float* weights, int32_t* offsets,
-                                 int32_t* tokens, int32_t* positions, void* stream);
+                                 int32_t* tokens, int32_t* positions, void* ws, size_t ws_bytes,
+                                 void* stream);
 
 /*
  * spmm24_f8_grouped -- spmm24_f8 for E weights of the same shape, each with rows

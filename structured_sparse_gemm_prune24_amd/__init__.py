@@ -130,7 +130,8 @@ _F8_SIGNATURES = {
 # entry points declared in include/prune24_experts.h
 _EXPERTS_SIGNATURES = {
     "experts_route": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i32, _c_vp, _c_i32, ctypes.c_float, _c_vp,
-                               _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
+                               _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
+    "experts_route_workspace": (_c_size, [_c_i64, _c_i64]),
     "spmm24_f8_grouped": (_c_i32, [_c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64,
                                    _c_vp, _c_i32, _c_i64, _c_vp, _c_i32, _c_vp]),
     "experts_combine": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp,

@@ -1,13 +1,17 @@
 // Routing of tokens to experts, and the combination of a token's experts.
 //
 // Routing: the k best of E logits per token, then a counting sort of the T k
-// choices by expert.  The sort uses no atomics and no scratch memory: for each
-// expert one block reads all choices (from the L2; 256 KiB for 8192 tokens of 8),
-// counts those of lower experts, which gives the expert's first row, and ranks
-// its own in token order.  That is E times the reading that a histogram in two
-// launches would do, and one launch less.
+// choices by expert, without atomics on memory.  Which of 32 tokens chose an expert
+// is one word, whose bits count the expert's rows and rank them in token order.
+// The first launch picks and leaves the counts of each 32 tokens; in the second
+// every group adds up the counts ahead of it (from the L2: T / 32 x E) and places
+// its rows.  Past 8192 tokens a launch between them sums the counts once for all;
+// up to 64 tokens one launch does everything.
+// Bound by instructions: about 90 for each choice of four tokens.
 //
 // Combination: bound by HBM, T (k + 2) rows.
+#include <type_traits>
+
 #include "../../include/prune24_experts.h"
 #include "p24_api_internal.hpp"
 #include "p24_f8.hpp"
@@ -23,6 +27,7 @@ struct RouteArgs {
   int* offsets;
   int* tokens;
   int* positions;
+  int* counts;       // groups of 32 tokens x E, and a row of sums
   int T, E, k;
   int score, normalize;
   float scale;
@@ -30,52 +35,42 @@ struct RouteArgs {
 
 // Keys whose unsigned order is the order of the scores: NaN above +inf, -0 as +0.  No score has key 0.
 __device__ __forceinline__ uint32_t score_key(float v) {
-  if (v != v) return 0xFFFFFFFFu;
   const uint32_t u = __float_as_uint(v + 0.0f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return v != v ? 0xFFFFFFFFu : k;
 }
 __device__ __forceinline__ uint64_t score_key(double v) {
-  if (v != v) return ~0ull;
   const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
-  return u >> 63 ? ~u : u | 1ull << 63;
+  const uint64_t k = u >> 63 ? ~u : u | 1ull << 63;
+  return v != v ? ~0ull : k;
 }
 
-// Reductions over the G lanes of a token, 16 or all 64, the result in each: quads, mirrored halves and
-// rows of 16, then the wave's four rows.
+// Reductions over the 16 lanes of a token, the result in each: quads, then mirrored halves and rows.
+constexpr int G = 16;
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, true);
 }
 constexpr int SWAP1 = 0xB1, SWAP2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140;   // quad_perm 1 0 3 2, 2 3 0 1, ..
-template <int G, typename F>
+template <typename F>
 __device__ __forceinline__ uint32_t reduce(uint32_t v, F&& f) {
-  static_assert(G == 16 || G == 64, "a row of lanes, or a wave");
   v = f(v, dpp<SWAP1>(v));
   v = f(v, dpp<SWAP2>(v));
   v = f(v, dpp<HALF_MIRROR>(v));
-  v = f(v, dpp<MIRROR>(v));
-  if constexpr (G == 64) {
-    v = f(v, (uint32_t)__shfl_xor((int)v, 16));
-    v = f(v, (uint32_t)__shfl_xor((int)v, 32));
-  }
-  return v;
+  return f(v, dpp<MIRROR>(v));
 }
-template <int G>
 __device__ __forceinline__ uint32_t max_of(uint32_t v) {
-  return reduce<G>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+  return reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-template <int G>
 __device__ __forceinline__ uint32_t min_of(uint32_t v) {
-  return reduce<G>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+  return reduce(v, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
-template <int G>
 __device__ __forceinline__ uint64_t max_of(uint64_t v) {
-  const uint32_t hi = max_of<G>((uint32_t)(v >> 32));
-  return (uint64_t)hi << 32 | max_of<G>((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  const uint32_t hi = max_of((uint32_t)(v >> 32));
+  return (uint64_t)hi << 32 | max_of((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
 }
-template <int G>
 __device__ __forceinline__ float sum_of(float v) {
-  return __uint_as_float(reduce<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+  return __uint_as_float(reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
@@ -83,239 +78,353 @@ __device__ __forceinline__ float sum_of(float v) {
 __device__ __forceinline__ float logit_at(const uint16_t* row, int e) { return __uint_as_float((uint32_t)row[e] << 16); }
 __device__ __forceinline__ float logit_at(const float* row, int e) { return row[e]; }
 
-// One token on G lanes, V experts each (4 G c + 4 lane + [0, 4) for c < V / 4).  Slot j's expert and weight
-// end up in lane j % G, entry j / G.
-template <typename T, typename Key, int G, int V>
+// What ranks an expert with a bias: in 64 bits, or (T float) to within 2^-22 of max(1, |score|): the exponent's
+// roundings, |x| 2^-23 of exp(x), weigh |x| s (1 - s) < 1/4 in the sigmoid s, exp2 and the reciprocal one ulp each.
+template <typename T>
+__device__ __forceinline__ T biased_score(float logit, float bias) {
+  if constexpr (sizeof(T) == 8) return 1.0 / (1.0 + exp(-(double)logit)) + (double)bias;
+  else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(logit * -1.44269504088896341f)) + bias;
+}
+
+// The k best keys of one token on 16 lanes, V experts each (64 c + 4 lane + [0, 4) for c < V / 4): slot j's expert
+// ends up in lane j % 16, entry j / 16; `first` is the best.  Key 0 is no expert.  With CHECK the k + 1 best are
+// picked, and the result says what cannot be told apart: NEAR two neighbours among them, EDGE the last and the one behind it.
+enum { NEAR = 1, EDGE = 2 };
+template <int V, bool CHECK, typename Key>
+__device__ __forceinline__ int pick(Key (&key)[V], int k, int (&expert)[2], int& first) {
+  const int lane = threadIdx.x % G;
+  expert[0] = expert[1] = -1;
+  first = -1;
+  int unsure = 0;
+  float last = 0.0f;
+  for (int j = 0; j < k + (CHECK ? 2 : 0); ++j) {
+    Key best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    const Key top = max_of(best);
+    if (top == 0) break;       // of all the token's lanes alike
+    if constexpr (CHECK) {
+      const float score = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+      if (j > 0 && !(last - score > 0x1p-20f * fmaxf(1.0f, fmaxf(fabsf(last), fabsf(score))))) unsure |= j <= k ? NEAR : EDGE;
+      last = score;
+      if (j > k) break;
+    }
+    int at = V;                // the lane's lowest expert of that key
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) at = key[v] == top ? v : at;
+    const uint32_t mine = at < V ? (uint32_t)(64 * (at / 4) + 4 * lane + at % 4) : 0xFFFFFFFFu;
+    const uint32_t e = min_of(mine);
+    at = mine == e ? at : V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = at == v ? 0 : key[v];
+    if (j == 0) first = (int)e;
+    if (lane == j % G) {
+      if (j < G) expert[0] = (int)e;
+      else if (j < 2 * G) expert[1] = (int)e;
+    }
+  }
+  return unsure;
+}
+
+// Lane j's expert and key, j < 16, into descending order of the keys (ties: the lower expert); -1 is no expert.
+__device__ __forceinline__ int in_order(int expert, uint64_t key) {
+  const int lane = threadIdx.x % G;
+  int rank = 0, out = -1;
+  for (int i = 0; i < G; ++i) {
+    const int e = __shfl(expert, i, G);
+    const uint64_t k = (uint64_t)(uint32_t)__shfl((int)(key >> 32), i, G) << 32 | (uint32_t)__shfl((int)key, i, G);
+    rank += e >= 0 && (k > key || (k == key && e < expert));
+  }
+  if (expert < 0) rank = G;
+  for (int i = 0; i < G; ++i) {
+    const int e = __shfl(expert, i, G), r = __shfl(rank, i, G);
+    out = r == lane ? e : out;
+  }
+  return out;
+}
+
+// One token: its slots' experts and weights, in the lanes of pick.  BIAS: sigmoid and bias.  64-bit exponentials of all
+// scores take as long as all the rest (8192 tokens of 256 experts: 14.3 us, 10.8 this way), so 32 bits pick one
+// expert more than asked for; where those cannot tell two of them apart, one token in some hundreds, 64 bits put
+// them in order, and only where the edge of what was picked is unsure too, everything is done in 64.
+template <typename T, bool BIAS, int V>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int (&expert)[2], float (&weight)[2]) {
-  constexpr bool WIDE = sizeof(Key) == 8;   // sigmoid and bias
   const int lane = threadIdx.x % G;
   const T* row = (const T*)a.logits + t * a.ldl;
-  Key key[V];
-  float l[WIDE ? 1 : V];
+  float l[V];
 #pragma unroll
   for (int c = 0; c < V / 4; ++c) {
     const int e = 4 * G * c + 4 * lane;
-    float x[4], b[4];
+    float x[4];
     load_row<4>(row + e, a.E - e, x);
-    if constexpr (WIDE) load_row<4>(a.bias + e, a.E - e, b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool open = e + i < a.E && x[i] != -INFINITY;
-      if constexpr (WIDE) {
-        key[4 * c + i] = open ? score_key(1.0 / (1.0 + exp(-(double)x[i])) + (double)b[i]) : 0;
-      } else {
-        key[4 * c + i] = open ? score_key(x[i]) : 0;
-        l[4 * c + i] = open ? x[i] : -INFINITY;
-      }
-    }
-    if constexpr (WIDE) __builtin_amdgcn_sched_barrier(0);   // four exponentials at a time: their registers
+    for (int i = 0; i < 4; ++i) l[4 * c + i] = e + i < a.E ? x[i] : -INFINITY;
   }
-  expert[0] = expert[1] = -1;
-  int first = -1;    // the best expert
-  for (int j = 0; j < a.k; ++j) {
-    Key best = 0;
-    int at = 0;
+  int first;    // the best expert
+  auto biased = [&](auto KEY, auto CHECK) {
+    typedef decltype(KEY) Key;
+    typedef std::conditional_t<sizeof(Key) == 8, double, float> Score;
+    Key key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (key[v] > best) {     // the lower of equals
-        best = key[v];
-        at = v;
+    for (int c = 0; c < V / 4; ++c) {
+      const int e = 4 * G * c + 4 * lane;
+      float b[4];
+      load_row<4>(a.bias + e, a.E - e, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Key score = score_key(biased_score<Score>(l[4 * c + i], b[i]));     // of all: a branch for each would wait for each
+        key[4 * c + i] = l[4 * c + i] == -INFINITY ? 0 : score;
+      }
+      __builtin_amdgcn_sched_barrier(0);   // four exponentials at a time: their registers
+    }
+    return pick<V, decltype(CHECK)::value>(key, a.k, expert, first);
+  };
+  if constexpr (BIAS) {
+    const int unsure = biased(uint32_t{}, std::true_type{});
+    if (unsure & NEAR) {
+      if (a.k < G && !(unsure & EDGE)) {
+        const int e = max(expert[0], 0);
+        const uint64_t key = score_key(biased_score<double>(logit_at(row, e), a.bias[e]));
+        expert[0] = in_order(expert[0], key);
+        first = __shfl(expert[0], 0, G);
+      } else {
+        biased(uint64_t{}, std::false_type{});
       }
     }
-    const int mine = 4 * G * (at / 4) + 4 * lane + at % 4;
-    const Key top = max_of<G>(best);
-    if (top == 0) break;       // of all the token's lanes alike
-    const int e = (int)min_of<G>(best == top ? (uint32_t)mine : 0xFFFFFFFFu);
+    if (lane >= a.k) expert[0] = -1;      // the one more
+    if (lane + G >= a.k) expert[1] = -1;
+  } else {
+    uint32_t key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (4 * G * (v / 4) + 4 * lane + v % 4 == e) key[v] = 0;
-    if (j == 0) first = e;
-    if (lane == j % G) {
-      if (j < G) expert[0] = e;
-      else expert[1] = e;
-    }
+    for (int v = 0; v < V; ++v) key[v] = l[v] == -INFINITY ? 0 : score_key(l[v]);
+    pick<V, false>(key, a.k, expert, first);
   }
   // weights, from the logits themselves
   float w[2] = {0.0f, 0.0f};
-  float all = 0.0f;
+  float all = 1.0f;
   if (a.score == P24_SCORE_SOFTMAX) {
     const float top = first >= 0 ? logit_at(row, first) : 0.0f;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (expert[s] >= 0) w[s] = expf(logit_at(row, expert[s]) - top);
-    if constexpr (!WIDE) {
-      if (!a.normalize) {
+    if (!a.normalize) {
+      all = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) all += expf(l[v] - top);   // closed ones: exp(-inf)
-        all = sum_of<G>(all);
+      for (int v = 0; v < V; ++v) {
+        const float p = expf(l[v] - top);
+        all += l[v] == -INFINITY ? 0.0f : p;
       }
+      all = sum_of(all);
     }
   } else {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (expert[s] >= 0) w[s] = 1.0f / (1.0f + expf(-logit_at(row, expert[s])));
-    all = 1.0f;
   }
-  if (a.normalize) all = sum_of<G>(w[0] + w[1]);
+  if (a.normalize) all = sum_of(w[0] + w[1]);
 #pragma unroll
   for (int s = 0; s < 2; ++s) weight[s] = expert[s] >= 0 ? w[s] / all * a.scale : 0.0f;
 }
 
-template <typename T, typename Key, int G, int V>
-__global__ __launch_bounds__(256) void k_route_top(const RouteArgs a) {
-  const int t = blockIdx.x * (256 / G) + threadIdx.x / G, lane = threadIdx.x % G;
-  if (t >= a.T) return;
-  int e[2];
-  float w[2];
-  route_token<T, Key, G, V>(a, t, e, w);
+constexpr int GROUP = 32;       // tokens whose choices are counted together
+constexpr int FEW = 64;         // tokens that one block takes
+constexpr int SLOTS = P24_EXPERTS_MAX;
+
+// base[e] = rows of lower experts + ahead[e], from the experts' rows total[e] (LDS); the sums alone to `offsets`, if
+// given.  All threads of the block.  Returns the number of rows in all.
+__device__ __forceinline__ int scan_experts(int* base, const int* total, const int* ahead, int E, int* offsets) {
+  __shared__ int waves[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, count = blockDim.x >> 6;
+  int carry = 0;
+  for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x, mine = e < E ? total[e] : 0;
+    int upto = mine;
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (G * s + lane < a.k) {
-      a.experts[(int64_t)t * a.k + G * s + lane] = e[s];
-      a.weights[(int64_t)t * a.k + G * s + lane] = w[s];
+    for (int o = 1; o < 64; o <<= 1) {
+      const int other = __shfl_up(upto, o);
+      upto += lane >= o ? other : 0;
     }
+    if (lane == 63) waves[wave] = upto;
+    __syncthreads();
+    int before = carry, sum = 0;
+    for (int w = 0; w < count; ++w) {
+      before += w < wave ? waves[w] : 0;
+      sum += waves[w];
+    }
+    if (e < E) {
+      base[e] = before + upto - mine + (ahead ? ahead[e] : 0);
+      if (offsets) offsets[e] = before + upto - mine;
+    }
+    carry += sum;
+    __syncthreads();
+  }
+  if (offsets && threadIdx.x == 0) offsets[E] = carry;
+  return carry;
 }
 
-// A few tokens in one block: T k <= 512 choices, each ranked against all others in LDS.
-constexpr int FEW = 512;
-template <typename T, typename Key, int G, int V>
-__global__ __launch_bounds__(512) void k_route_few(const RouteArgs a) {
-  __shared__ __attribute__((aligned(16))) int id[FEW];     // slots without an expert rank last
-  const int n = a.T * a.k, lane = threadIdx.x % G;
-  for (int i = n + threadIdx.x; i < FEW; i += blockDim.x) id[i] = INT32_MAX;
-  for (int t = threadIdx.x / G; t < a.T; t += blockDim.x / G) {
+// The rows of tokens t0 on, one bit each of `chosen`, from the experts' bases.
+template <typename Word>
+__device__ __forceinline__ void place_rows(const RouteArgs& a, int t0, const Word* chosen, const int* base) {
+  const int n = min(a.T - t0, (int)sizeof(Word) * 8) * a.k;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int64_t slot = (int64_t)t0 * a.k + i;
+    const int e = a.experts[slot], t = i / a.k;
+    int at = -1;
+    if (e >= 0) {
+      at = base[e] + __popcll(chosen[e] & (((Word)1 << t) - 1));
+      a.tokens[at] = t0 + t;
+    }
+    a.positions[slot] = at;
+  }
+}
+// Rows from `rows` on have no token.
+__device__ __forceinline__ void no_tokens(const RouteArgs& a, int rows, int thread, int threads) {
+  for (int i = rows + thread; i < a.T * a.k; i += threads) a.tokens[i] = -1;
+}
+
+// Picks the experts of tokens t0 on and sets their bits (LDS; the order does not matter).
+template <typename T, bool BIAS, int V, typename Word>
+__device__ __forceinline__ void pick_group(const RouteArgs& a, int t0, Word* chosen) {
+  const int lane = threadIdx.x % G;
+  for (int t = threadIdx.x / G; t < min(a.T - t0, (int)sizeof(Word) * 8); t += blockDim.x / G) {
     int e[2];
     float w[2];
-    route_token<T, Key, G, V>(a, t, e, w);
+    route_token<T, BIAS, V>(a, t0 + t, e, w);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (G * s + lane < a.k) {
-        const int i = t * a.k + G * s + lane;
+        const int64_t i = (int64_t)(t0 + t) * a.k + G * s + lane;
         a.experts[i] = e[s];
         a.weights[i] = w[s];
-        id[i] = e[s] < 0 ? INT32_MAX : e[s];
+        if (e[s] >= 0) atomicOr(&chosen[e[s]], (Word)1 << t);
       }
   }
+}
+
+// 32 tokens a block: picks, and counts the rows.
+template <typename T, bool BIAS, int V>
+__global__ __launch_bounds__(512) void k_route_pick(const RouteArgs a) {
+  __shared__ unsigned chosen[SLOTS];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) chosen[e] = 0;
   __syncthreads();
+  pick_group<T, BIAS, V>(a, blockIdx.x * GROUP, chosen);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = __popc(chosen[e]);
+}
+
+// 64 tokens at most, in one block.
+template <typename T, bool BIAS, int V>
+__global__ __launch_bounds__(512) void k_route_few(const RouteArgs a) {
+  __shared__ unsigned long long chosen[SLOTS];
+  __shared__ int base[SLOTS], total[SLOTS];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) chosen[e] = 0;
+  __syncthreads();
+  pick_group<T, BIAS, V>(a, 0, chosen);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) total[e] = __popcll(chosen[e]);
+  __syncthreads();
+  const int rows = scan_experts(base, total, nullptr, a.E, a.offsets);
+  place_rows(a, 0, chosen, base);     // reads the experts that this block wrote: barriers lie between
+  no_tokens(a, rows, threadIdx.x, blockDim.x);
+}
+
+// The counts of 64 experts a block: each group's become those of the groups ahead of it, their sums the last row.
+// The block's 16 waves take a run of groups each.
+__global__ __launch_bounds__(1024) void k_route_sum(const RouteArgs a, int groups) {
+  constexpr int WAVES = 16;
+  __shared__ int part[WAVES][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
+  const int run = (groups + WAVES - 1) / WAVES, g0 = min(wave * run, groups), g1 = min(g0 + run, groups);
+  int* const col = a.counts + e;
+  int sum = 0;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int g = g0; g < g1; ++g) sum += col[(int64_t)g * a.E];
+  }
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (e >= a.E) return;
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) before += w < wave ? part[w][lane] : 0;
+#pragma unroll 8
+  for (int g = g0; g < g1; ++g) {
+    const int c = col[(int64_t)g * a.E];
+    col[(int64_t)g * a.E] = before;
+    before += c;
+  }
+  if (wave == WAVES - 1) col[(int64_t)groups * a.E] = before;
+}
+
+// The rows of 32 tokens a block.  SUMMED: k_route_sum has run.
+template <bool SUMMED>
+__global__ __launch_bounds__(1024) void k_route_place(const RouteArgs a) {
+  __shared__ unsigned chosen[SLOTS];
+  __shared__ int base[SLOTS], total[SLOTS], ahead[SLOTS];
+  const int t0 = blockIdx.x * GROUP, groups = gridDim.x, E = a.E;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    chosen[e] = 0;
+    total[e] = SUMMED ? a.counts[(int64_t)groups * E + e] : 0;
+    ahead[e] = SUMMED ? a.counts[(int64_t)blockIdx.x * E + e] : 0;
+  }
+  __syncthreads();
+  const int n = min(a.T - t0, GROUP) * a.k;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int mine = id[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += id[j] < mine || (id[j] == mine && j < i);
-    a.positions[i] = mine == INT32_MAX ? -1 : rank;
-    a.tokens[rank] = mine == INT32_MAX ? -1 : i / a.k;
+    const int e = a.experts[(int64_t)t0 * a.k + i];
+    if (e >= 0) atomicOr(&chosen[e], 1u << (i / a.k));
   }
-  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
-    int below = 0;
-    for (int j = 0; j < n; ++j) below += id[j] < e;
-    a.offsets[e] = below;
-  }
-}
-
-// Block e of E + 1: expert e's offset and rows; the last one the slots without an expert.  The block's 16
-// waves each take a run of the choices in order, 256 at a time (four a lane); a lane keeps which of
-// its first 64 are the expert's, and reads those past them again.
-__global__ __launch_bounds__(1024) void k_route_sort(const RouteArgs a) {
-  constexpr int WAVES = 16, KEPT = 16;
-  __shared__ int below_of[WAVES], mine_of[WAVES];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const bool rest = (int)blockIdx.x == a.E;
-  const int target = rest ? -1 : (int)blockIdx.x;
-  const int n = a.T * a.k;
-  const int rounds = ((n + 255) / 256 + WAVES - 1) / WAVES;      // of a wave
-  const int first = wave * rounds * 256;
-  auto matches = [&](int r, int& below) {
-    const int i = first + r * 256 + 4 * lane;
-    int id[4] = {-2, -2, -2, -2};
-    if (i + 4 <= n) {
-      const int4 v = *reinterpret_cast<const int4*>(a.experts + i);
-      id[0] = v.x;
-      id[1] = v.y;
-      id[2] = v.z;
-      id[3] = v.w;
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u < n) id[u] = a.experts[i + u];
+  if constexpr (!SUMMED) {
+    // the groups' counts, several runs of groups side by side; the parts meet in LDS (whole numbers: any order)
+    const int width = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : E <= 512 ? 512 : 1024;
+    const int parts = 1024 / width, part = threadIdx.x / width, e = threadIdx.x % width;
+    if (e < E) {
+      int sum = 0, before = 0;
+#pragma unroll 8
+      for (int g = part; g < groups; g += parts) {
+        const int c = a.counts[(int64_t)g * E + e];
+        sum += c;
+        before += g < (int)blockIdx.x ? c : 0;
+      }
+      atomicAdd(&total[e], sum);
+      atomicAdd(&ahead[e], before);
     }
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      m |= (uint32_t)(id[u] == target) << u;
-      below += rest ? id[u] >= 0 : (id[u] >= 0 && id[u] < target);
-    }
-    return m;
-  };
-  int below = 0, mine = 0;
-  uint64_t kept = 0;
-#pragma unroll 4
-  for (int r = 0; r < rounds; ++r) {
-    const uint32_t m = matches(r, below);
-    mine += __popc(m);
-    if (r < KEPT) kept |= (uint64_t)m << (4 * r);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    below += __shfl_xor(below, o);
-    mine += __shfl_xor(mine, o);
-  }
-  if (lane == 0) {
-    below_of[wave] = below;
-    mine_of[wave] = mine;
   }
   __syncthreads();
-  int start = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    start += below_of[w];
-    before += w < wave ? mine_of[w] : 0;
-  }
-  if (threadIdx.x == 0) a.offsets[blockIdx.x] = start;
-  int row = start + before;
-  for (int r = 0; r < rounds && mine; ++r) {
-    int unused = 0;
-    const uint32_t m = r < KEPT ? (uint32_t)(kept >> (4 * r)) & 15u : matches(r, unused);
-    uint64_t who[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) who[u] = __ballot(m >> u & 1);
-    const uint64_t ahead = (1ull << lane) - 1;
-    int at = row;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      at += __popcll(who[u] & ahead);
-      row += __popcll(who[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (m >> u & 1) {
-        const int i = first + r * 256 + 4 * lane + u;
-        a.tokens[at] = rest ? -1 : i / a.k;
-        a.positions[i] = rest ? -1 : at;
-        ++at;
-      }
-    }
-  }
+  const int rows = scan_experts(base, total, ahead, E, blockIdx.x == 0 ? a.offsets : nullptr);
+  place_rows(a, t0, chosen, base);
+  no_tokens(a, rows, blockIdx.x * 1024 + threadIdx.x, groups * 1024);
 }
 
-template <typename T, typename Key, int G, int V>
+static int64_t route_groups(int64_t T) { return (T + GROUP - 1) / GROUP; }
+
+template <typename T, bool BIAS, int V>
 static p24_status launch_route(const RouteArgs& a, hipStream_t st) {
-  if ((int64_t)a.T * a.k <= FEW) {
-    const int threads = a.T >= 16 || a.E > 256 ? 512 : 256;
-    hipLaunchKernelGGL((k_route_few<T, Key, G, V>), dim3(1), dim3(threads), 0, st, a);
+  if (a.T <= FEW) {
+    hipLaunchKernelGGL((k_route_few<T, BIAS, V>), dim3(1), dim3(a.T <= 16 ? 256 : 512), 0, st, a);
     return launch_status();
   }
-  hipLaunchKernelGGL((k_route_top<T, Key, G, V>), dim3((unsigned)(((int64_t)a.T * G + 255) / 256)), dim3(256), 0, st, a);
-  const p24_status s = launch_status();
+  const unsigned groups = (unsigned)route_groups(a.T);
+  hipLaunchKernelGGL((k_route_pick<T, BIAS, V>), dim3(groups), dim3(512), 0, st, a);
+  p24_status s = launch_status();
   if (s != P24_OK) return s;
-  hipLaunchKernelGGL(k_route_sort, dim3((unsigned)a.E + 1), dim3(1024), 0, st, a);
+  if (groups <= 256) {
+    hipLaunchKernelGGL(k_route_place<false>, dim3(groups), dim3(1024), 0, st, a);
+    return launch_status();
+  }
+  hipLaunchKernelGGL(k_route_sum, dim3((unsigned)(a.E + 63) / 64), dim3(1024), 0, st, a, (int)groups);
+  s = launch_status();
+  if (s != P24_OK) return s;
+  hipLaunchKernelGGL(k_route_place<true>, dim3(groups), dim3(1024), 0, st, a);
   return launch_status();
 }
 
-template <typename T, typename Key>
+template <typename T, bool BIAS>
 static p24_status route_by_experts(const RouteArgs& a, hipStream_t st) {
-  if (a.E <= 64) return launch_route<T, Key, 16, 4>(a, st);
-  if (a.E <= 128) return launch_route<T, Key, 16, 8>(a, st);
-  if (a.E <= 256) return launch_route<T, Key, 16, 16>(a, st);
-  return launch_route<T, Key, 64, 16>(a, st);
+  if (a.E <= 64) return launch_route<T, BIAS, 4>(a, st);
+  if (a.E <= 128) return launch_route<T, BIAS, 8>(a, st);
+  if (a.E <= 256) return launch_route<T, BIAS, 16>(a, st);
+  if (a.E <= 512) return launch_route<T, BIAS, 32>(a, st);
+  return launch_route<T, BIAS, 64>(a, st);
 }
 
 struct CombineArgs {
@@ -384,10 +493,14 @@ static size_t float_bytes(int32_t d) { return d == P24_F32 ? 4 : 2; }
 
 using namespace p24;
 
+extern "C" P24_API size_t experts_route_workspace(int64_t T, int64_t E) {
+  return T <= FEW || E < 1 ? 0 : (size_t)(route_groups(T) + 1) * (size_t)E * 4;
+}
+
 extern "C" P24_API p24_status experts_route(const void* logits, int32_t l_dtype, int64_t ldl, int64_t T, int64_t E,
                                             int64_t k, int32_t score, const float* bias, int32_t normalize, float scale,
                                             int32_t* experts, float* weights, int32_t* offsets, int32_t* tokens,
-                                            int32_t* positions, void* stream) {
+                                            int32_t* positions, void* ws, size_t ws_bytes, void* stream) {
   if (!float_type(l_dtype)) return P24_ERR_DTYPE;
   if (T < 0 || E < 1 || k < 1 || k > E || ldl < E || !(scale - scale == 0.0f)) return P24_ERR_SHAPE;
   if (score != P24_SCORE_SOFTMAX && score != P24_SCORE_SIGMOID) return P24_ERR_UNSUPPORTED;
@@ -395,9 +508,14 @@ extern "C" P24_API p24_status experts_route(const void* logits, int32_t l_dtype,
   if (E > P24_EXPERTS_MAX || k > P24_EXPERTS_K_MAX || T > (1 << 18)) return P24_ERR_UNSUPPORTED;
   if (!offsets || (T && (!logits || !experts || !weights || !tokens || !positions))) return P24_ERR_NULL;
   if (!aligned(offsets, 4) || !aligned(logits, float_bytes(l_dtype)) || !aligned(weights, 4) || !aligned(tokens, 4) ||
-      !aligned(positions, 4) || !aligned(experts, 16) || (bias && !aligned(bias, 4)))
+      !aligned(positions, 4) || !aligned(experts, 4) || (bias && !aligned(bias, 4)))
     return P24_ERR_ALIGN;
+  const size_t need = experts_route_workspace(T, E);
+  if (need && !ws) return P24_ERR_NULL;
+  if (need && !aligned(ws, 4)) return P24_ERR_ALIGN;
+  if (ws_bytes < need) return P24_ERR_WORKSPACE;
   RouteArgs a{};
+  a.counts = (int*)ws;
   a.logits = logits;
   a.ldl = ldl;
   a.bias = bias;
@@ -413,8 +531,8 @@ extern "C" P24_API p24_status experts_route(const void* logits, int32_t l_dtype,
   a.normalize = normalize != 0;
   a.scale = scale;
   const hipStream_t st = (hipStream_t)stream;
-  if (l_dtype == P24_F32) return bias ? route_by_experts<float, uint64_t>(a, st) : route_by_experts<float, uint32_t>(a, st);
-  return bias ? route_by_experts<uint16_t, uint64_t>(a, st) : route_by_experts<uint16_t, uint32_t>(a, st);
+  if (l_dtype == P24_F32) return bias ? route_by_experts<float, true>(a, st) : route_by_experts<float, false>(a, st);
+  return bias ? route_by_experts<uint16_t, true>(a, st) : route_by_experts<uint16_t, false>(a, st);
 }
 
 extern "C" P24_API p24_status experts_combine(const void* Z, int32_t z_dtype, int64_t ldz, int64_t rows,

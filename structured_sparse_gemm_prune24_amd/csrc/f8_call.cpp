@@ -29,6 +29,7 @@ decltype(&rms_norm) p_norm = nullptr;
 decltype(&gated_act) p_gate = nullptr;
 decltype(&spmm24_f8) p_product = nullptr;
 decltype(&experts_route) p_route = nullptr;
+decltype(&experts_route_workspace) p_route_ws = nullptr;
 decltype(&spmm24_f8_grouped) p_grouped = nullptr;
 decltype(&experts_combine) p_combine = nullptr;
 decltype(&quantize_f8_block) p_quantize = nullptr;
@@ -244,14 +245,16 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float* bias = nullptr;
     if (!is_none(a[3]) && !(bias = vec(a[3], E, dev))) return none();
     const int64_t each = (T * k + 3) / 4 * 4;
-    const at::Tensor buf = make({4 * (4 * each + E + 1)}, at::kByte, dev);
+    const int64_t ws = 4 * each + E + 1, need = (int64_t)p_route_ws(T, E);      // the workspace lies behind the outputs
+    const at::Tensor buf = make({4 * ws + need}, at::kByte, dev);
     const at::Tensor experts = part_of(buf, at::kInt, {T, k}, 0), weights = part_of(buf, at::kFloat, {T, k}, each),
                      tokens = part_of(buf, at::kInt, {T * k}, 2 * each), positions = part_of(buf, at::kInt, {T, k}, 3 * each),
                      offsets = part_of(buf, at::kInt, {E + 1}, 4 * each);
     const p24_status st =
         p_route(l->data_ptr(), code, ldl, T, E, k, (int)PyLong_AsLong(a[2]), bias, (int)PyLong_AsLong(a[4]),
                 (float)PyFloat_AS_DOUBLE(a[5]), (int32_t*)experts.data_ptr(), (float*)weights.data_ptr(),
-                (int32_t*)offsets.data_ptr(), (int32_t*)tokens.data_ptr(), (int32_t*)positions.data_ptr(), stream_of(dev));
+                (int32_t*)offsets.data_ptr(), (int32_t*)tokens.data_ptr(), (int32_t*)positions.data_ptr(),
+                (int32_t*)buf.data_ptr() + ws, (size_t)need, stream_of(dev));
     if (st != P24_OK) return none();
     return give_all({&experts, &weights, &offsets, &tokens, &positions});
   });
@@ -363,11 +366,11 @@ PyObject* block_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // bind(rms_norm, gated_act, spmm24_f8, experts_route, spmm24_f8_grouped, experts_combine, quantize_f8_block,
-// gemm_f8_block): their addresses
+// gemm_f8_block, experts_route_workspace): their addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int COUNT = 8;
+  constexpr int COUNT = 9;
   if (n != COUNT) {
-    PyErr_SetString(PyExc_TypeError, "bind takes eight addresses");
+    PyErr_SetString(PyExc_TypeError, "bind takes nine addresses");
     return nullptr;
   }
   void* p[COUNT];
@@ -383,6 +386,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p_combine = reinterpret_cast<decltype(p_combine)>(p[5]);
   p_quantize = reinterpret_cast<decltype(p_quantize)>(p[6]);
   p_block = reinterpret_cast<decltype(p_block)>(p[7]);
+  p_route_ws = reinterpret_cast<decltype(p_route_ws)>(p[8]);
   Py_RETURN_NONE;
 }
 

@@ -96,11 +96,12 @@ def route(logits, k: int, score="softmax", bias=None, normalize=True, scale=1.0)
         raise ValueError("a bias goes with score \"sigmoid\"")
     bp = None if bias is None else _vector(bias, "bias", E, dev)
     new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+    ws = torch.empty(lib().experts_route_workspace(T, E), dtype=torch.uint8, device=dev)
     r = Routing(new(T, k), torch.empty((T, k), dtype=torch.float32, device=dev), new(E + 1), new(T * k), new(T, k))
     with torch.cuda.device(dev):
         _check(lib().experts_route(logits.data_ptr(), _CODES[logits.dtype], ldl, T, E, k, code, bp, int(bool(normalize)),
                                    scale, r.experts.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
-                                   r.tokens.data_ptr(), r.positions.data_ptr(),
+                                   r.tokens.data_ptr(), r.positions.data_ptr(), ws.data_ptr(), ws.numel(),
                                    torch.cuda.current_stream(dev).cuda_stream), "experts_route")
     return r
 

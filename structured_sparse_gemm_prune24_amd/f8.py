@@ -61,7 +61,7 @@ def _call():
                                "or python structured_sparse_gemm_prune24_amd/build.py") from e
         c.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                  for f in (L.rms_norm, L.gated_act, L.spmm24_f8, L.experts_route, L.spmm24_f8_grouped, L.experts_combine,
-                           L.quantize_f8_block, L.gemm_f8_block)))
+                           L.quantize_f8_block, L.gemm_f8_block, L.experts_route_workspace)))
         _CALL = c
     return _CALL
 

@@ -88,7 +88,7 @@ def _check_route(logits, k, score="softmax", bias=None, normalize=True, scale=1.
     return r
 
 
-ROUTES = [(1, 1, 1), (1, 128, 8), (3, 5, 5), (7, 64, 6), (40, 60, 4), (63, 8, 8), (64, 257, 3), (65, 512, 16), (33, 1000, 32),
+ROUTES = [(1, 1, 1), (1, 128, 8), (3, 5, 5), (7, 64, 6), (40, 60, 4), (63, 8, 8), (64, 257, 3), (64, 1024, 32), (8195, 5, 2), (9000, 130, 3), (65, 512, 16), (33, 1000, 32),
           (200, 256, 8), (513, 16, 2), (1000, 31, 7), (2050, 128, 1), (300, 1024, 17)]
 
 
@@ -407,3 +407,25 @@ def test_graph_and_streams():
         sy = p24.feed_forward_f8_experts(xq, l, 3, wgu, wd, residual=h)
     side.synchronize()
     assert torch.equal(sy, y)
+
+
+@pytest.mark.parametrize("T", [20, 400])
+def test_route_of_scores_that_32_bits_cannot_tell_apart(T):
+    """Sigmoid and bias: experts whose scores differ by less than an fp32 step, at the edge of the chosen and among
+    them, and far too many of them; saturated sigmoids tie in 64 bits too and go to the lower expert."""
+    need_gpu()
+    bias = torch.zeros(64, device="cuda")
+    l = _randn(5, T, 64)
+    step = torch.arange(64, device="cuda") * 1e-7
+    l[0] = 3.0 + step                       # all of them near
+    l[1] = 3.0 - step
+    l[2, 10:14] = 4.0 + step[:4]            # a few among the chosen
+    l[3, 40:42] = torch.tensor([4.0, 4.0000005], device="cuda")
+    l[4] = 50.0                             # sigmoid 1 in 64 bits: ties
+    l[5, ::2] = 40.0 + step[::2]
+    order = torch.sort(l[6], descending=True).indices
+    l[6, order[5]] = l[6, order[4]] - 1e-6  # across the edge of k = 5
+    l[7, order[6]] = l[7].max() + 1         # and one that is just behind it
+    for k in (5, 6, 15, 16, 20):
+        _check_route(l, k, score="sigmoid", bias=bias)
+        _check_route(l, k, score="sigmoid", bias=bias - 1000.0)     # the bias swallows the sigmoid's last bits in 32
