@@ -58,12 +58,12 @@ __global__ __launch_bounds__(W * 64) void k_f8_tokens_grouped(const F8GroupedArg
 template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
 __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8_grouped(const F8GroupedArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[f8_lds_bytes<BM, BN, WGM, WGN, LW, KG, OutT>()];
-  const uint32_t nbm = g.a.nbm, tiles = F8GroupSearch<BN>(g.groups).total() * nbm;
+  F8GroupSearch<BN> search(g.groups);
+  const uint32_t nbm = g.a.nbm, tiles = search.total() * nbm;
   for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x) {
     const uint32_t b = xcd_remap(i, tiles);
     int expert, first, count;
     uint32_t first_tile, bm, bn;
-    F8GroupSearch<BN> search(g.groups);       // anew: its registers are the tile's
     if (!search.find(b / nbm, expert, first, count, first_tile)) return;   // (never: b < tiles)
     f8_place(b - first_tile * nbm, nbm, F8GroupSearch<BN>::tiles_of(count), bm, bn);
     F8RowMap rows;

@@ -271,7 +271,9 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
   const int lane = thread & 63, h = lane >> 5;
   const int wave_id = __builtin_amdgcn_readfirstlane(thread >> 6);
   const int kg = KG == 1 ? 0 : wave_id / C::GWAVES, wave = KG == 1 ? wave_id : wave_id % C::GWAVES;
-  const int wm = wave / WGN, wn = wave % WGN;
+  // GROUPED: every other row of waves takes the tokens from the far end, so that the two waves of a SIMD (w and
+  // w + 4) have different ones, and a tile of few tokens leaves each SIMD one of the waves that have some.
+  const int wm = wave / WGN, wn = GROUPED && wm % 2 ? WGN - 1 - wave % WGN : wave % WGN;
   uint8_t* lds = lds_all + kg * (NSTAGE * C::STAGE);     // this group's stages
 
   const int64_t ldx = args.ldx;
@@ -500,12 +502,26 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
       else __builtin_amdgcn_s_barrier();        // the other groups' last step
     }
   };
-  if (loader) loop(I1{});
+  // a wave without tokens loads and keeps step
+  auto idle = [&]() {
+    uint32_t st = 0;
+    for (int it = 0; it < nk / KG; ++it) {
+      if (loader) wait_steps(std::integral_constant<int, NSTAGE - 2>{});
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (loader) static_for<0, C::DMA>([&](auto Q) { issue(Q, it + NSTAGE, st, std::false_type{}); });
+      st = st == (NSTAGE - 1) * C::STAGE ? 0 : st + C::STAGE;
+    }
+  };
+  static_assert(!GROUPED || KG == 1, "idle waves keep step with one group");
+  if (GROUPED && wn * C::WTN >= n_rows) idle();
+  else if (loader) loop(I1{});
   else loop(I0{});
 
   wait_loads<0>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  if (GROUPED && wn * C::WTN >= n_rows) return;
 
   if constexpr (INPLACE) {
     // Epilogue in place: every value is finished in the accumulators' order,
