@@ -45,6 +45,11 @@ __device__ __forceinline__ uint64_t score_key(double v) {
   return v != v ? ~0ull : k;
 }
 
+// The score of a key.
+__device__ __forceinline__ float key_score(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
 // Reductions over the 16 lanes of a token, the result in each: quads, then mirrored halves and rows.
 constexpr int G = 16;
 template <int CTRL>
@@ -87,14 +92,14 @@ __device__ __forceinline__ T biased_score(float logit, float bias) {
 }
 
 // The k best keys of one token on 16 lanes, V experts each (64 c + 4 lane + [0, 4) for c < V / 4): slot j's expert
-// ends up in lane j % 16, entry j / 16; `first` is the best.  Key 0 is no expert.  With CHECK the k + 1 best are
+// and key end up in lane j % 16, entry j / 16; `first` is the best's key.  Key 0 is no expert.  With CHECK the k + 1 best are
 // picked, and the result says what cannot be told apart: NEAR two neighbours among them, EDGE the last and the one behind it.
 enum { NEAR = 1, EDGE = 2 };
 template <int V, bool CHECK, typename Key>
-__device__ __forceinline__ int pick(Key (&key)[V], int k, int (&expert)[2], int& first) {
+__device__ __forceinline__ int pick(Key (&key)[V], int k, int (&expert)[2], Key (&chosen)[2], Key& first) {
   const int lane = threadIdx.x % G;
   expert[0] = expert[1] = -1;
-  first = -1;
+  chosen[0] = chosen[1] = first = 0;
   int unsure = 0;
   float last = 0.0f;
   for (int j = 0; j < k + (CHECK ? 2 : 0); ++j) {
@@ -104,7 +109,7 @@ __device__ __forceinline__ int pick(Key (&key)[V], int k, int (&expert)[2], int&
     const Key top = max_of(best);
     if (top == 0) break;       // of all the token's lanes alike
     if constexpr (CHECK) {
-      const float score = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+      const float score = key_score(top);
       if (j > 0 && !(last - score > 0x1p-20f * fmaxf(1.0f, fmaxf(fabsf(last), fabsf(score))))) unsure |= j <= k ? NEAR : EDGE;
       last = score;
       if (j > k) break;
@@ -117,10 +122,15 @@ __device__ __forceinline__ int pick(Key (&key)[V], int k, int (&expert)[2], int&
     at = mine == e ? at : V;
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = at == v ? 0 : key[v];
-    if (j == 0) first = (int)e;
+    if (j == 0) first = top;
     if (lane == j % G) {
-      if (j < G) expert[0] = (int)e;
-      else if (j < 2 * G) expert[1] = (int)e;
+      if (j < G) {
+        expert[0] = (int)e;
+        chosen[0] = top;
+      } else if (j < 2 * G) {
+        expert[1] = (int)e;
+        chosen[1] = top;
+      }
     }
   }
   return unsure;
@@ -160,7 +170,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int (&exp
 #pragma unroll
     for (int i = 0; i < 4; ++i) l[4 * c + i] = e + i < a.E ? x[i] : -INFINITY;
   }
-  int first;    // the best expert
+  float at[2] = {0.0f, 0.0f}, top = 0.0f;    // the chosen logits, and the largest (softmax)
   auto biased = [&](auto KEY, auto CHECK) {
     typedef decltype(KEY) Key;
     typedef std::conditional_t<sizeof(Key) == 8, double, float> Score;
@@ -177,7 +187,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int (&exp
       }
       __builtin_amdgcn_sched_barrier(0);   // four exponentials at a time: their registers
     }
-    return pick<V, decltype(CHECK)::value>(key, a.k, expert, first);
+    Key chosen[2], first;
+    return pick<V, decltype(CHECK)::value>(key, a.k, expert, chosen, first);
   };
   if constexpr (BIAS) {
     const int unsure = biased(uint32_t{}, std::true_type{});
@@ -186,27 +197,34 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int (&exp
         const int e = max(expert[0], 0);
         const uint64_t key = score_key(biased_score<double>(logit_at(row, e), a.bias[e]));
         expert[0] = in_order(expert[0], key);
-        first = __shfl(expert[0], 0, G);
       } else {
         biased(uint64_t{}, std::false_type{});
       }
     }
     if (lane >= a.k) expert[0] = -1;      // the one more
     if (lane + G >= a.k) expert[1] = -1;
-  } else {
-    uint32_t key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = l[v] == -INFINITY ? 0 : score_key(l[v]);
-    pick<V, false>(key, a.k, expert, first);
+    for (int s = 0; s < 2; ++s)
+      if (expert[s] >= 0) at[s] = logit_at(row, expert[s]);
+  } else {
+    uint32_t key[V], chosen[2], first;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t score = score_key(l[v]);
+      key[v] = l[v] == -INFINITY ? 0 : score;
+    }
+    pick<V, false>(key, a.k, expert, chosen, first);
+    at[0] = key_score(chosen[0]);
+    at[1] = key_score(chosen[1]);
+    top = key_score(first);
   }
   // weights, from the logits themselves
   float w[2] = {0.0f, 0.0f};
   float all = 1.0f;
   if (a.score == P24_SCORE_SOFTMAX) {
-    const float top = first >= 0 ? logit_at(row, first) : 0.0f;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      if (expert[s] >= 0) w[s] = expf(logit_at(row, expert[s]) - top);
+      if (expert[s] >= 0) w[s] = expf(at[s] - top);
     if (!a.normalize) {
       all = 0.0f;
 #pragma unroll
@@ -219,7 +237,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int (&exp
   } else {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      if (expert[s] >= 0) w[s] = 1.0f / (1.0f + expf(-logit_at(row, expert[s])));
+      if (expert[s] >= 0) w[s] = 1.0f / (1.0f + expf(-at[s]));
   }
   if (a.normalize) all = sum_of(w[0] + w[1]);
 #pragma unroll
@@ -262,13 +280,14 @@ __device__ __forceinline__ int scan_experts(int* base, const int* total, const i
   return carry;
 }
 
-// The rows of tokens t0 on, one bit each of `chosen`, from the experts' bases.
+// The rows of tokens t0 on, one bit each of `chosen`, from the experts' bases; `experts`: their choices.
 template <typename Word>
-__device__ __forceinline__ void place_rows(const RouteArgs& a, int t0, const Word* chosen, const int* base) {
+__device__ __forceinline__ void place_rows(const RouteArgs& a, int t0, const int* experts, const Word* chosen,
+                                           const int* base) {
   const int n = min(a.T - t0, (int)sizeof(Word) * 8) * a.k;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int64_t slot = (int64_t)t0 * a.k + i;
-    const int e = a.experts[slot], t = i / a.k;
+    const int e = experts[i], t = i / a.k;
     int at = -1;
     if (e >= 0) {
       at = base[e] + __popcll(chosen[e] & (((Word)1 << t) - 1));
@@ -284,7 +303,7 @@ __device__ __forceinline__ void no_tokens(const RouteArgs& a, int rows, int thre
 
 // Picks the experts of tokens t0 on and sets their bits (LDS; the order does not matter).
 template <typename T, bool BIAS, int V, typename Word>
-__device__ __forceinline__ void pick_group(const RouteArgs& a, int t0, Word* chosen) {
+__device__ __forceinline__ void pick_group(const RouteArgs& a, int t0, Word* chosen, int* copy = nullptr) {
   const int lane = threadIdx.x % G;
   for (int t = threadIdx.x / G; t < min(a.T - t0, (int)sizeof(Word) * 8); t += blockDim.x / G) {
     int e[2];
@@ -296,6 +315,7 @@ __device__ __forceinline__ void pick_group(const RouteArgs& a, int t0, Word* cho
         const int64_t i = (int64_t)(t0 + t) * a.k + G * s + lane;
         a.experts[i] = e[s];
         a.weights[i] = w[s];
+        if (copy) copy[t * a.k + G * s + lane] = e[s];
         if (e[s] >= 0) atomicOr(&chosen[e[s]], (Word)1 << t);
       }
   }
@@ -316,15 +336,15 @@ __global__ __launch_bounds__(512) void k_route_pick(const RouteArgs a) {
 template <typename T, bool BIAS, int V>
 __global__ __launch_bounds__(512) void k_route_few(const RouteArgs a) {
   __shared__ unsigned long long chosen[SLOTS];
-  __shared__ int base[SLOTS], total[SLOTS];
+  __shared__ int base[SLOTS], total[SLOTS], experts[FEW * P24_EXPERTS_K_MAX];
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) chosen[e] = 0;
   __syncthreads();
-  pick_group<T, BIAS, V>(a, 0, chosen);
+  pick_group<T, BIAS, V>(a, 0, chosen, experts);
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) total[e] = __popcll(chosen[e]);
   __syncthreads();
   const int rows = scan_experts(base, total, nullptr, a.E, a.offsets);
-  place_rows(a, 0, chosen, base);     // reads the experts that this block wrote: barriers lie between
+  place_rows(a, 0, experts, chosen, base);
   no_tokens(a, rows, threadIdx.x, blockDim.x);
 }
 
@@ -391,7 +411,7 @@ __global__ __launch_bounds__(1024) void k_route_place(const RouteArgs a) {
   }
   __syncthreads();
   const int rows = scan_experts(base, total, ahead, E, blockIdx.x == 0 ? a.offsets : nullptr);
-  place_rows(a, t0, chosen, base);
+  place_rows(a, t0, a.experts + (int64_t)t0 * a.k, chosen, base);
   no_tokens(a, rows, blockIdx.x * 1024 + threadIdx.x, groups * 1024);
 }
 
