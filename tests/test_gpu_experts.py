@@ -429,3 +429,52 @@ def test_route_of_scores_that_32_bits_cannot_tell_apart(T):
     for k in (5, 6, 15, 16, 20):
         _check_route(l, k, score="sigmoid", bias=bias)
         _check_route(l, k, score="sigmoid", bias=bias - 1000.0)     # the bias swallows the sigmoid's last bits in 32
+
+
+def test_offsets_past_32_bits():
+    """Outputs and combined rows of more than 2^31 elements: the last rows are those of a small call."""
+    need_gpu()
+    M, n = 32768, 70000
+    c = _weights(5, 2, M, 64)
+    x = _x(6, n, 64)
+    y = p24.spmm24_f8_grouped(c, x, _offsets([30000, 40000]))
+    small = p24.Quantized8(x.values[-5:], x.scale[-5:].contiguous())
+    want = p24.spmm24_f8_grouped(c, small, _offsets([0, 5]))
+    assert (y[-5:].float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max()     # another kernel's sums
+    assert want.any()
+    pos = torch.arange(n - 1, n - 7, -1, dtype=torch.int32, device="cuda").reshape(3, 2)
+    w = torch.rand(3, 2, generator=_gen(1), device="cuda")
+    assert torch.equal(p24.combine_experts(y, pos, w), p24.combine_experts(y[-6:], pos - (n - 6), w))
+
+
+def test_two_streams_at_once():
+    """Two layers on two streams: no state between calls."""
+    need_gpu()
+    a, b = _layer(40, 300, 256, 192, 12), _layer(60, 200, 256, 192, 8)
+    want = [p24.feed_forward_f8_experts(xq, l, 3, wgu, wd, residual=h) for xq, h, l, wgu, wd in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, (xq, h, l, wgu, wd) in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(p24.feed_forward_f8_experts(xq, l, 3, wgu, wd, residual=h))
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_example(monkeypatch, capsys):
+    """The example runs and is near the fp64 layer: its output is rounded to bf16 twice (2^-8 of a value each at most),
+    and what the layer adds to the residual, under a fiftieth of it at these weights (0.02 times the square root of
+    256 and 192 inputs: values of 0.3 times 0.16, then 0.02), is 0.15 off at most by two 8-bit operands."""
+    need_gpu()
+    import os
+    import runpy
+    import sys
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "experts_f8.py")
+    monkeypatch.setattr(sys, "argv", [path, "--tokens", "5", "--width", "256", "--hidden", "192", "--experts", "8", "--k", "2",
+                                      "--steps", "2"])
+    runpy.run_path(path, run_name="__main__")
+    line = capsys.readouterr().out
+    assert "5 tokens, 2 of 8 experts 256 -> 192 -> 256" in line
+    assert float(line.split("error")[1]) <= 2 * 2.0 ** -8 + 0.15 / 50

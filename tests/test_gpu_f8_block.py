@@ -318,3 +318,26 @@ def test_graph_and_streams():
         sy, _ = p24.feed_forward_f8_block(x, r, g, w1, w2)
     side.synchronize()
     assert torch.equal(sy, y)
+
+
+def test_offsets_past_32_bits():
+    """An output, and an input, of more than 2^31 elements: the last rows are those of a small call."""
+    need_gpu()
+    M, N = 32768, 70000
+    w = p24.quantize_weight_f8_block(0.02 * _randn(1, M, 32))
+    x = p24.quantize_f8_block(_randn(2, N, 32))
+    y = p24.gemm_f8_block(w, x)
+    want = p24.gemm_f8_block(w, p24.Rows8Block(x.values[-70:], x.scale[:, -70:]))
+    assert torch.equal(y[-70:], want) and want.any()
+    q = p24.quantize_f8_block(y)
+    few = p24.quantize_f8_block(y[-5:])
+    assert torch.equal(q.values[-5:].view(torch.uint8), few.values.view(torch.uint8)) and torch.equal(q.scale[:, -5:], few.scale)
+
+
+@pytest.mark.parametrize("N,M,K", [(8, 5, 1 << 20), (200, 130, 65536 + 16)])
+def test_long_k(N, M, K):
+    need_gpu()
+    w = p24.quantize_weight_f8_block(0.02 * _randn(1, M, K))
+    x = p24.quantize_f8_block(_randn(2, N, K))
+    for out in (torch.bfloat16, torch.float32):
+        _check_product(w, x, out=out)
