@@ -81,7 +81,7 @@ P24_API p24_status experts_route(const void* logits, int32_t l_dtype, int64_t ld
  *   bias      E x M fp32, or NULL.  act as for spmm24_f8.
  *   1 <= E <= P24_EXPERTS_MAX; rows, M and K as N, M and K of spmm24_f8.
  * Sums are those of spmm24_f8: exact products and fp32 sums for P24_F32 outputs,
- * the 8-bit matrix unit's for P24_BF16.
+ * the 8-bit matrix unit's for P24_BF16.  P24_F8_TILE forces a kernel, as there.
  */
 P24_API p24_status spmm24_f8_grouped(const void* data, const float* w_scale, int64_t E, int64_t M,
                                      int64_t K, const void* X, int64_t ldx, const float* x_scale,

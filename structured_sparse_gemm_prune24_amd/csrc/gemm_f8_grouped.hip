@@ -106,25 +106,26 @@ static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
 
 // Which kernel.  Where the rows lie is not known here: the experts' numbers of rows are taken as
 // exponentially distributed, so that an expert with a rows on average has 1 / (1 - exp(-BN / a)) tiles of BN rows.
-// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp): over 70 shapes drawn at
-// random it is 1.6 % behind the fastest of the eight for bf16 outputs, 1.3 % for fp32 (geometric mean).
+// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp): over 160 shapes drawn at
+// random it is 2.8 % behind the fastest of the eight for bf16 outputs, 2.3 % for fp32 (geometric mean).
 // Measured, us (T tokens of k experts, of E with M x K):
-//   4096 of 8, 64 of 4096 x 2048   256x256 234, 256x192 249, 256x128 269, 128x128 320, 64x64 496
-//   1024 of 8, 64 of 4096 x 2048   256x192 102, 256x128 106, 128x128 117, 256x256 120
-//   256 of 8, 128 of 2048 x 2048   128x64 65, 256x128 68, 64x32 72, tokens 116
+//   4096 of 8, 64 of 4096 x 2048   256x256 241, 256x192 264, 256x128 282, 128x128 331, 64x64 512
+//   2048 of 8, 128 of 2048 x 2048  256x128 110, 256x256 112, 128x128 115, 256x192 120, 64x64 168
+//   512 of 2, 8 of 4096 x 4096     256x128 23.2, 256x192 25.9, 128x128 27.9, 64x32 38.7
+//   1571 of 2, 7 of 1000 x 1088    128x128 11.1, 128x64 11.6, 64x64 13.5; fp32 15.6, 16.3, 18.0
 //   64 of 4, 32 of 4096 x 4096     64x32 59, 128x64 59, 64x64 64, tokens 73
 //   1 of 8, 128 of 2048 x 4096     tokens 9.1, 64x32 13.6
 enum F8GroupedKernel { G_TOKENS, G_64x32, G_64x64, G_128x64, G_128x128, G_256x128, G_256x192, G_256x256, G_KERNELS };
 
 constexpr TileCost GROUPED_BF16[G_KERNELS] = {
-    {32, 32, 3.96, 0.064, 0.42, 0.139},  {64, 32, 5.50, 0.250, 0.85, 0.149},   {64, 64, 5.65, 0.255, 1.10, 0.180},
-    {128, 64, 5.56, 0.257, 1.95, 0.327}, {128, 128, 6.20, 0.319, 3.01, 0.378}, {256, 128, 7.05, 0.407, 5.78, 0.797},
-    {256, 192, 8.12, 0.502, 6.14, 1.08}, {256, 256, 9.03, 0.681, 8.10, 1.08},
+    {32, 32, 4.02, 0.066, 0.46, 0.137},  {64, 32, 5.83, 0.237, 0.74, 0.157},   {64, 64, 5.85, 0.221, 0.95, 0.186},
+    {128, 64, 5.84, 0.232, 1.77, 0.346}, {128, 128, 6.35, 0.269, 2.40, 0.387}, {256, 128, 7.32, 0.358, 5.17, 0.773},
+    {256, 192, 8.45, 0.438, 6.43, 0.832}, {256, 256, 9.28, 0.564, 7.47, 0.861},
 };
 // (the widened operands of an fp32 output do not fit the registers of the two widest)
 constexpr TileCost GROUPED_F32[G_256x192] = {
-    {32, 32, 4.17, 0.074, 0.45, 0.151},  {64, 32, 5.37, 0.480, 1.00, 0.178},   {64, 64, 5.60, 0.461, 1.38, 0.237},
-    {128, 64, 5.75, 0.463, 2.67, 0.385}, {128, 128, 6.58, 0.541, 3.97, 0.575}, {256, 128, 7.36, 0.869, 8.26, 1.07},
+    {32, 32, 4.21, 0.088, 0.49, 0.145},  {64, 32, 5.86, 0.471, 0.96, 0.177},   {64, 64, 5.85, 0.441, 1.27, 0.213},
+    {128, 64, 6.05, 0.440, 2.42, 0.388}, {128, 128, 6.39, 0.451, 3.29, 0.445}, {256, 128, 7.27, 0.831, 7.14, 1.03},
 };
 
 static F8GroupedKernel choose_grouped(const F8GroupedArgs& g, bool exact) {
