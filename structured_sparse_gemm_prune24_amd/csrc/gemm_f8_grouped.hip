@@ -106,8 +106,9 @@ static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
 
 // Which kernel.  Where the rows lie is not known here: the experts' numbers of rows are taken as
 // exponentially distributed, so that an expert with a rows on average has 1 / (1 - exp(-BN / a)) tiles of BN rows.
-// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp): over 160 shapes drawn at
-// random it is 2.8 % behind the fastest of the eight for bf16 outputs, 2.3 % for fp32 (geometric mean).
+// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp).  Over 160 shapes drawn at random
+// it is 2.9 % behind the fastest, over 60 large ones (256 to 8192 tokens, 512 to 4096 k) 3.9 % for bf16 outputs and
+// 2.6 % for fp32 (geometric means).
 // Measured, us (T tokens of k experts, of E with M x K):
 //   4096 of 8, 64 of 4096 x 2048   256x256 241, 256x192 264, 256x128 282, 128x128 331, 64x64 512
 //   2048 of 8, 128 of 2048 x 2048  256x128 110, 256x256 112, 128x128 115, 256x192 120, 64x64 168
@@ -118,14 +119,14 @@ static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
 enum F8GroupedKernel { G_TOKENS, G_64x32, G_64x64, G_128x64, G_128x128, G_256x128, G_256x192, G_256x256, G_KERNELS };
 
 constexpr TileCost GROUPED_BF16[G_KERNELS] = {
-    {32, 32, 4.02, 0.066, 0.46, 0.137},  {64, 32, 5.83, 0.237, 0.74, 0.157},   {64, 64, 5.85, 0.221, 0.95, 0.186},
-    {128, 64, 5.84, 0.232, 1.77, 0.346}, {128, 128, 6.35, 0.269, 2.40, 0.387}, {256, 128, 7.32, 0.358, 5.17, 0.773},
-    {256, 192, 8.45, 0.438, 6.43, 0.832}, {256, 256, 9.28, 0.564, 7.47, 0.861},
+    {32, 32, 4.02, 0.066, 0.46, 0.137},  {64, 32, 5.83, 0.237, 0.66, 0.138},   {64, 64, 5.85, 0.221, 0.93, 0.160},
+    {128, 64, 5.84, 0.232, 1.75, 0.283}, {128, 128, 6.35, 0.269, 2.33, 0.369}, {256, 128, 7.32, 0.358, 4.63, 0.739},
+    {256, 192, 8.45, 0.438, 7.60, 0.798}, {256, 256, 9.28, 0.564, 6.87, 0.976},
 };
 // (the widened operands of an fp32 output do not fit the registers of the two widest)
 constexpr TileCost GROUPED_F32[G_256x192] = {
-    {32, 32, 4.21, 0.088, 0.49, 0.145},  {64, 32, 5.86, 0.471, 0.96, 0.177},   {64, 64, 5.85, 0.441, 1.27, 0.213},
-    {128, 64, 6.05, 0.440, 2.42, 0.388}, {128, 128, 6.39, 0.451, 3.29, 0.445}, {256, 128, 7.27, 0.831, 7.14, 1.03},
+    {32, 32, 4.21, 0.088, 0.49, 0.145},  {64, 32, 5.86, 0.471, 0.85, 0.165},   {64, 64, 5.85, 0.441, 1.27, 0.220},
+    {128, 64, 6.05, 0.440, 2.20, 0.390}, {128, 128, 6.39, 0.451, 3.61, 0.511}, {256, 128, 7.27, 0.831, 7.15, 1.02},
 };
 
 static F8GroupedKernel choose_grouped(const F8GroupedArgs& g, bool exact) {
