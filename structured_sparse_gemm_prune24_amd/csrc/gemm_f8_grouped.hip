@@ -57,18 +57,47 @@ __global__ __launch_bounds__(W * 64) void k_f8_tokens_grouped(const F8GroupedArg
 
 template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
 __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8_grouped(const F8GroupedArgs g) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[f8_lds_bytes<BM, BN, WGM, WGN, LW, KG, OutT>()];
+  using C = F8Tile<BM, BN, WGM, WGN, LW, KG>;
+  constexpr bool CHAIN = f8_chained<BM, BN, WGM, WGN, LW, KG, OutT>();
+  __shared__ __attribute__((aligned(1024)))
+  uint8_t lds[f8_lds_bytes<BM, BN, WGM, WGN, LW, KG, OutT>() + (CHAIN ? F8Chain<C>::TOKENS : 0)];
   F8GroupSearch<BN> search(g.groups);
   const uint32_t nbm = g.a.nbm, tiles = search.total() * nbm;
-  for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x) {
-    const uint32_t b = xcd_remap(i, tiles);
+  struct Tile {
     int expert, first, count;
-    uint32_t first_tile, bm, bn;
-    if (!search.find(b / nbm, expert, first, count, first_tile)) return;   // (never: b < tiles)
-    f8_place(b - first_tile * nbm, nbm, F8GroupSearch<BN>::tiles_of(count), bm, bn);
+    uint32_t bm, bn;
+  };
+  auto find = [&](uint32_t i, Tile& t) {
+    const uint32_t b = xcd_remap(i, tiles);
+    uint32_t first_tile;
+    if (!search.find(b / nbm, t.expert, t.first, t.count, first_tile)) return false;   // (never: b < tiles)
+    f8_place(b - first_tile * nbm, nbm, F8GroupSearch<BN>::tiles_of(t.count), t.bm, t.bn);
+    return true;
+  };
+  F8Chain<C> chain;
+  Tile tile;
+  uint32_t i = blockIdx.x;
+  if (i >= tiles || !find(i, tile)) return;
+  for (;;) {
+    i += gridDim.x;
+    Tile next = tile;
+    const bool more = i < tiles && find(i, next);
     F8RowMap rows;
-    const F8Args a = f8_part<OutT>(g, expert, first, count, rows);
-    f8_block_tile<BM, BN, WGM, WGN, LW, KG, OutT, true>(a, lds, (int)bm * BM, (int)bn * BN, rows);
+    const F8Args a = f8_part<OutT>(g, tile.expert, tile.first, tile.count, rows);
+    if constexpr (CHAIN) {
+      F8RowMap next_rows;
+      const F8Args n = f8_part<OutT>(g, next.expert, next.first, next.count, next_rows);
+      chain.more = more;
+      chain.W = n.W;
+      chain.X = n.X;
+      chain.tokens = next_rows.tokens;
+      chain.N = n.N;
+      chain.m0 = (int)next.bm * BM;
+      chain.n0 = (int)next.bn * BN;
+    }
+    f8_block_tile<BM, BN, WGM, WGN, LW, KG, OutT, true, CHAIN>(a, lds, (int)tile.bm * BM, (int)tile.bn * BN, rows, &chain);
+    if (!more) return;
+    tile = next;
     // the next tile's loads go where this one's epilogue reads
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -106,22 +135,26 @@ static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
 
 // Which kernel.  Where the rows lie is not known here: the experts' numbers of rows are taken as
 // exponentially distributed, so that an expert with a rows on average has 1 / (1 - exp(-BN / a)) tiles of BN rows.
-// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp).  Over 160 shapes drawn at random
-// it is 2.9 % behind the fastest, over 60 large ones (256 to 8192 tokens, 512 to 4096 k) 3.9 % for bf16 outputs and
-// 2.6 % for fp32 (geometric means).
+// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp).  Over 79 shapes of 256 to 32768
+// rows drawn at random it is 2.4 % behind the fastest, over 60 large ones (256 to 8192 tokens, 512 to 4096 k) 3.6 %
+// (fp32 outputs: 2.9 % over 160 shapes, 2.6 %; geometric means).
 // Measured, us (T tokens of k experts, of E with M x K):
-//   4096 of 8, 64 of 4096 x 2048   256x256 241, 256x192 264, 256x128 282, 128x128 331, 64x64 512
-//   2048 of 8, 128 of 2048 x 2048  256x128 110, 256x256 112, 128x128 115, 256x192 120, 64x64 168
-//   512 of 2, 8 of 4096 x 4096     256x128 23.2, 256x192 25.9, 128x128 27.9, 64x32 38.7
+//   4096 of 8, 64 of 4096 x 2048   256x256 232, 256x192 250, 256x128 273, 128x128 316, 64x64 512
+//   2048 of 8, 128 of 2048 x 2048  256x256 103, 256x128 110, 128x128 115, 256x192 120, 64x64 168
+//   512 of 2, 8 of 4096 x 4096     256x128 23.3, 256x192 26.5, 128x128 28.3, 64x32 38.7
 //   1571 of 2, 7 of 1000 x 1088    128x128 11.1, 128x64 11.6, 64x64 13.5; fp32 15.6, 16.3, 18.0
 //   64 of 4, 32 of 4096 x 4096     64x32 59, 128x64 59, 64x64 64, tokens 73
 //   1 of 8, 128 of 2048 x 4096     tokens 9.1, 64x32 13.6
+//
+// What bounds the largest (measured inside the kernel, 256x256 of the first line): a tile takes 21.5 us, 15 of them its 16
+// steps, 4.4 its epilogue, 1.8 the start of the next.  A step takes as long without the multiplies (0.85 us for its 52 KB
+// a CU, 0.65 without the loads): the way from the L2 to LDS is the bound, hits or not (0.9 with every weight there).
 enum F8GroupedKernel { G_TOKENS, G_64x32, G_64x64, G_128x64, G_128x128, G_256x128, G_256x192, G_256x256, G_KERNELS };
 
 constexpr TileCost GROUPED_BF16[G_KERNELS] = {
     {32, 32, 4.02, 0.066, 0.46, 0.137},  {64, 32, 5.83, 0.237, 0.66, 0.138},   {64, 64, 5.85, 0.221, 0.93, 0.160},
-    {128, 64, 5.84, 0.232, 1.75, 0.283}, {128, 128, 6.35, 0.269, 2.33, 0.369}, {256, 128, 7.32, 0.358, 4.63, 0.739},
-    {256, 192, 8.45, 0.438, 7.60, 0.798}, {256, 256, 9.28, 0.564, 6.87, 0.976},
+    {128, 64, 5.84, 0.232, 1.75, 0.283}, {128, 128, 6.35, 0.269, 2.33, 0.369}, {256, 128, 11.4, 0.322, 5.73, 0.748},
+    {256, 192, 12.6, 0.428, 6.70, 0.858}, {256, 256, 12.2, 0.574, 6.95, 0.944},
 };
 // (the widened operands of an fp32 output do not fit the registers of the two widest)
 constexpr TileCost GROUPED_F32[G_256x192] = {

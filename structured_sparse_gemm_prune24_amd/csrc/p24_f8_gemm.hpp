@@ -201,6 +201,12 @@ __device__ __forceinline__ int lds_b32(uint32_t addr) {
   asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
   return v;
 }
+// a read that is waited for at once
+__device__ __forceinline__ int lds_b32_now(const void* p) {
+  int v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"((uint32_t)(uintptr_t)(lds_void*)p) : "memory");
+  return v;
+}
 
 // The fragments of one 64-k block in a wave: weights, positions, tokens.
 template <int TM, int TN>
@@ -255,13 +261,36 @@ constexpr int f8_lds_bytes() {
   return KG * C::NSTAGE * C::STAGE + (sizeof(OutT) != 4 && KG == 1 ? C::SCALES : 0);
 }
 
+// A block that has a CU to itself and walks over tiles: the loads of a tile's last steps bring the first two steps of the
+// next one, and its epilogue keeps to the stage of its last step, so that they are on their way, and
+// the stores drain, while the other goes on (4096 tokens of 8 of 64 experts with 4096 x 2048: 244 -> 232 us;
+// 8192 of 8 of 64 with 2048 x 768 126 -> 112).
+template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
+constexpr bool f8_chained() {
+  return sizeof(OutT) != 4 && KG == 1 && 2 * f8_lds_bytes<BM, BN, WGM, WGN, LW, KG, OutT>() > 160 * 1024;
+}
+// What it takes from a tile to the next.
+template <class C>
+struct F8Chain {
+  static constexpr int TOKENS = C::X_SCALES * 4;   // LDS bytes behind the scales: the next tile's tokens
+  bool primed = false;               // its first two steps have landed,
+  uint32_t st = 0;                   // the first in the stage at this byte
+  uint32_t x_row[C::X_DMA];          // its rows of X
+  // the next tile
+  bool more;
+  const uint8_t *W, *X;
+  const int* tokens;
+  int N, m0, n0;
+};
+
 // One tile: rows m0 on and tokens n0 on.  GROUPED: as for f8_tokens_tile, without a residual; X's rows
 // then lie anywhere, at a 32-bit offset that a lane keeps for each of its loads.
-template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT, bool GROUPED>
+template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT, bool GROUPED, bool CHAIN = false>
 __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_all, const int m0, const int n0,
-                                              const F8RowMap rows) {
+                                              const F8RowMap rows, F8Chain<F8Tile<BM, BN, WGM, WGN, LW, KG>>* chain = nullptr) {
   using C = F8Tile<BM, BN, WGM, WGN, LW, KG>;
   constexpr bool EXACT = sizeof(OutT) == 4, INPLACE = !EXACT && KG == 1;
+  static_assert(!CHAIN || (GROUPED && INPLACE && C::NSTAGE == 3), "a chain's stages");
   constexpr int TM = C::TM, TN = C::TN, NSTAGE = C::NSTAGE;
   typedef F8Frags<TM, TN> Frags;
 
@@ -270,6 +299,9 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
   if constexpr (GROUPED) asm volatile("" : "+v"(thread));
   const int lane = thread & 63, h = lane >> 5;
   const int wave_id = __builtin_amdgcn_readfirstlane(thread >> 6);
+  // the same in all lanes, and known to be: else the loads would loop over their values
+  const bool primed = CHAIN && __builtin_amdgcn_readfirstlane(chain->primed);
+  const uint32_t st_first = CHAIN ? __builtin_amdgcn_readfirstlane(chain->st) : 0;
   const int kg = KG == 1 ? 0 : wave_id / C::GWAVES, wave = KG == 1 ? wave_id : wave_id % C::GWAVES;
   // GROUPED: every other row of waves takes the tokens from the far end, so that the two waves of a SIMD (w and
   // w + 4) have different ones, and a tile of few tokens leaves each SIMD one of the waves that have some.
@@ -285,7 +317,7 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
 
   const int n_rows = min(args.N - n0, BN);
   const bool gather = GROUPED && rows.tokens;
-  const __amdgpu_buffer_rsrc_t x_rsrc =
+  __amdgpu_buffer_rsrc_t x_rsrc =
       gather ? f8_rsrc(args.X, F8XReads<C>::bytes((int)rows.last + 1, ldx, args.K))
              : f8_rsrc(args.X + (int64_t)n0 * ldx, F8XReads<C>::bytes(n_rows, ldx, args.K));
   const F8XReads<C> x_reads(lane, wave, ldx, args.K);
@@ -293,14 +325,19 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
   uint32_t x_row[GROUPED ? C::X_DMA : 1], x_back = 0;
   if constexpr (GROUPED) {
     x_back = F8XReads<C>::back(F8XReads<C>::chunk(lane, wave), args.K);
+    if (primed) {
 #pragma unroll
-    for (int q = 0; q < C::X_DMA; ++q) {
-      const int r = min(F8XReads<C>::row(lane, wave, q), n_rows - 1);
-      x_row[q] = (uint32_t)(gather ? rows.template of<true>(n0 + r) : r) * (uint32_t)ldx + F8XReads<C>::chunk(lane, wave) * 16;
+      for (int q = 0; q < C::X_DMA; ++q) x_row[q] = chain->x_row[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < C::X_DMA; ++q) {
+        const int r = min(F8XReads<C>::row(lane, wave, q), n_rows - 1);
+        x_row[q] = (uint32_t)(gather ? rows.template of<true>(n0 + r) : r) * (uint32_t)ldx + F8XReads<C>::chunk(lane, wave) * 16;
+      }
     }
   }
   const F8WReads<C> w_reads(m0, args.M, args.K);
-  const __amdgpu_buffer_rsrc_t a_rsrc =
+  __amdgpu_buffer_rsrc_t a_rsrc =
       f8_rsrc(args.W + (int64_t)(m0 / 128) * steps * F8_PIECE, w_reads.bytes());
   uint32_t a_soff[C::A_DMA], a_dst[C::A_DMA];
 #pragma unroll
@@ -321,7 +358,7 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
     if constexpr (q < C::X_DMA) {
       uint32_t more = x_reads.rows(q);
       if constexpr (GROUPED) {
-        load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, x_row[q] - (g == nk - 1 ? x_back : 0), x_reads.scalar(g));
+        load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, x_row[q] - (x_back & (g == nk - 1 ? ~0u : 0u)), x_reads.scalar(g));
       } else if constexpr (decltype(WHOLE)::value) {
         load_to_lds(x_rsrc, stage + (q * C::LW + wave) * 1024, x_reads.vector(0, g == nk - 1), x_reads.scalar(g) + more);
       } else {
@@ -402,7 +439,8 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
   // The multiplies of one 64-k block, with the reads of the next one (block RSS
   // of the stage at byte rst) spread over their first three quarters and, where
   // LD, this wave's loads of step g into the stage at byte lst, one after each
-  // multiply (LD 1: operands, 2: the residual, 3: operands of a tile with no token past N).
+  // multiply (LD 1: operands, 2: the residual, 3: operands of a tile with no token past N,
+  // 4: the next tile's operands).
   auto block = [&](auto LD, const Frags& f, Frags& next, auto RSS, uint32_t rst, int g, uint32_t lst) {
     constexpr int NM = TM * TN, SPREAD = NM * 3 / 4 > 0 ? NM * 3 / 4 : 1;
     static_for<0, NM>([&](auto K) {
@@ -417,6 +455,7 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
       if constexpr (decltype(LD)::value == 1 && k < C::DMA) issue(K, g, lst, std::false_type{});
       if constexpr (decltype(LD)::value == 3 && k < C::DMA) issue(K, g, lst, std::true_type{});
       if constexpr (decltype(LD)::value == 2 && k < C::DMA) issue_residual(K, g, lst);
+      if constexpr (decltype(LD)::value == 4 && k < C::DMA) issue(K, g, lst, std::false_type{});
       constexpr int lo = k < SPREAD ? NR * k / SPREAD : NR, hi = k < SPREAD ? NR * (k + 1) / SPREAD : NR;
       static_for<lo, hi>([&](auto R) { read_one(RSS, R, rst, next); });
       __builtin_amdgcn_sched_barrier(0);
@@ -425,6 +464,7 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
       if constexpr (decltype(LD)::value == 1) issue(Q, g, lst, std::false_type{});
       if constexpr (decltype(LD)::value == 3) issue(Q, g, lst, std::true_type{});
       if constexpr (decltype(LD)::value == 2) issue_residual(Q, g, lst);
+      if constexpr (decltype(LD)::value == 4) issue(Q, g, lst, std::false_type{});
     });
   };
 
@@ -439,6 +479,9 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
     else wait_loads<n * (C::DMA - 1)>();
   };
   const bool residual_dma = INPLACE && !GROUPED && args.res_dma;
+  // (the next tile's tokens are there after two steps)
+  const bool link = CHAIN && __builtin_amdgcn_readfirstlane(chain->more && count >= 5);
+  uint8_t* next_tokens = lds_all + NSTAGE * C::STAGE + C::SCALES;
   if constexpr (INPLACE) {
     // scales and bias, 64 at a time, ahead of everything else
     uint8_t* sc = lds_all + NSTAGE * C::STAGE;
@@ -452,21 +495,36 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
       for (int u = wave; u < BM / 64; u += C::GWAVES) load4_to_lds(bs, sc + BM * 4 + u * 256, lane * 4 + u * 256, 0);
     for (int u = wave; u < C::X_SCALES / 64; u += C::GWAVES) {
       uint32_t at = lane * 4 + u * 256;
-      if (gather) at = (uint32_t)rows.template of<true>(n0 + min(lane + u * 64, n_rows - 1)) * 4;
+      if (gather && primed) {
+        // (past the tile's rows: some row of X)
+        at = min((uint32_t)lds_b32_now(next_tokens + at), rows.last) * 4;
+      } else if (gather) {
+        at = (uint32_t)rows.template of<true>(n0 + min(lane + u * 64, n_rows - 1)) * 4;
+      }
       load4_to_lds(xs, sc + BM * 8 + u * 256, at, 0);
+      if (CHAIN && link && chain->tokens)   // its own place, which no other wave reads before the next barrier
+        load4_to_lds(f8_rsrc((const uint8_t*)(chain->tokens + chain->n0), (uint32_t)min(chain->N - chain->n0, BN) * 4),
+                     next_tokens + u * 256, lane * 4 + u * 256, 0);
     }
   }
+  if (primed) {
+    if (loader)
+      static_for<0, C::DMA>([&](auto Q) {
+        issue(Q, 2, st_first == 0 ? 2 * C::STAGE : st_first - C::STAGE, std::false_type{});
+      });
+  } else {
 #pragma unroll
-  for (int g = 0; g < NSTAGE; ++g)
-    if (loader) {
-      if (residual_dma && g >= count) static_for<0, C::DMA>([&](auto Q) { issue_residual(Q, g, g * C::STAGE); });
-      else static_for<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE, std::false_type{}); });
-    }
-  wait_steps(std::integral_constant<int, NSTAGE - 1>{});
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+    for (int g = 0; g < NSTAGE; ++g)
+      if (loader) {
+        if (residual_dma && g >= count) static_for<0, C::DMA>([&](auto Q) { issue_residual(Q, g, g * C::STAGE); });
+        else static_for<0, C::DMA>([&](auto Q) { issue(Q, g, g * C::STAGE, std::false_type{}); });
+      }
+    wait_steps(std::integral_constant<int, NSTAGE - 1>{});
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
   Frags f0, f1;
-  static_for<0, NR>([&](auto R) { read_one(I0{}, R, 0, f0); });
+  static_for<0, NR>([&](auto R) { read_one(I0{}, R, st_first, f0); });
   f0.wait();
 
   // Step `it` lives in stage it % NSTAGE.  The barrier between its two 64-k
@@ -478,15 +536,47 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
     const uint32_t nx = st == (NSTAGE - 1) * C::STAGE ? 0 : st + C::STAGE;
     block(I0{}, f0, f1, I1{}, st, 0, 0);
     f1.wait();
-    if constexpr (decltype(LD)::value) wait_steps(std::integral_constant<int, NSTAGE - 2>{});
+    // (a primed tile's second step is there; the wait would be for the last tile's stores)
+    if constexpr (decltype(LD)::value)
+      if (!CHAIN || it > 0 || !primed) wait_steps(std::integral_constant<int, NSTAGE - 2>{});
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    block(LD, f1, f0, I0{}, nx, it + NSTAGE, st);
+    block(LD, f1, f0, I0{}, nx, decltype(LD)::value == 4 ? it + NSTAGE - count : it + NSTAGE, st);
     f0.wait();
     return nx;
   };
+  // the loads go on with the next tile
+  auto turn = [&]() {
+    const int n_next = min(chain->N - chain->n0, BN);
+    const bool gathered = chain->tokens != nullptr;
+    x_rsrc = gathered ? f8_rsrc(chain->X, F8XReads<C>::bytes((int)rows.last + 1, ldx, args.K))
+                      : f8_rsrc(chain->X + (int64_t)chain->n0 * ldx, F8XReads<C>::bytes(n_next, ldx, args.K));
+#pragma unroll
+    for (int q = 0; q < C::X_DMA; ++q) {
+      int r = min(F8XReads<C>::row(lane, wave, q), n_next - 1);
+      if (gathered) r = (int)min((uint32_t)lds_b32_now(next_tokens + r * 4), rows.last);
+      x_row[q] = (uint32_t)r * (uint32_t)ldx + F8XReads<C>::chunk(lane, wave) * 16;
+    }
+    const F8WReads<C> reads(chain->m0, args.M, args.K);
+    a_rsrc = f8_rsrc(chain->W + (int64_t)(chain->m0 / 128) * steps * F8_PIECE, reads.bytes());
+#pragma unroll
+    for (int j = 0; j < C::A_DMA; ++j) a_soff[j] = reads.scalar(j, wave);
+  };
+  uint32_t st_end = 0;    // the stage behind the last step's
   auto loop = [&](auto LD) {
+    if constexpr (CHAIN) {
+      uint32_t st = st_first;
+      int it = 0;
+      for (const int own = link ? count - NSTAGE : count - 1; it < own; ++it) st = body(LD, it, st);
+      if (link) {
+        if (decltype(LD)::value) turn();
+        for (; it < count - 1; ++it) st = body(std::integral_constant<int, decltype(LD)::value ? 4 : 0>{}, it, st);
+      }
+      // (the last step's stage is the epilogue's)
+      st_end = body(I0{}, count - 1, st);
+      return;
+    }
     const int common = nk / KG;
     const int plain = LD && residual_dma ? max(common - NSTAGE, 0) : common;
     uint32_t st = 0;
@@ -504,14 +594,20 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
   };
   // a wave without tokens loads and keeps step
   auto idle = [&]() {
-    uint32_t st = 0;
+    uint32_t st = st_first;
     for (int it = 0; it < nk / KG; ++it) {
-      if (loader) wait_steps(std::integral_constant<int, NSTAGE - 2>{});
+      if constexpr (CHAIN)
+        if (loader && link && it == count - NSTAGE) turn();
+      if (loader && (!CHAIN || it > 0 || !primed)) wait_steps(std::integral_constant<int, NSTAGE - 2>{});
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      if (loader) static_for<0, C::DMA>([&](auto Q) { issue(Q, it + NSTAGE, st, std::false_type{}); });
+      if (loader && (!CHAIN || it < count - 1))
+        static_for<0, C::DMA>([&](auto Q) {
+          issue(Q, CHAIN && link && it >= count - NSTAGE ? it + NSTAGE - count : it + NSTAGE, st, std::false_type{});
+        });
       st = st == (NSTAGE - 1) * C::STAGE ? 0 : st + C::STAGE;
     }
+    st_end = st;
   };
   static_assert(!GROUPED || KG == 1, "idle waves keep step with one group");
   if (GROUPED && wn * C::WTN >= n_rows) idle();
@@ -521,6 +617,12 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
   wait_loads<0>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  if constexpr (CHAIN) {
+    chain->primed = link;
+    chain->st = link ? st_end : 0;
+#pragma unroll
+    for (int q = 0; q < C::X_DMA; ++q) chain->x_row[q] = x_row[q];
+  }
   if (GROUPED && wn * C::WTN >= n_rows) return;
 
   if constexpr (INPLACE) {
@@ -528,19 +630,23 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
     // residual and rounding included, and goes into the wave's region as bf16;
     // whole rows of the region then go out 16 B a lane.
     const float* sc = reinterpret_cast<const float*>(lds_all + NSTAGE * C::STAGE);
-    uint8_t* region = lds_all + (count + wave / C::RPS) % NSTAGE * C::STAGE + wave % C::RPS * C::REGION;
+    // a slice: 32 tokens and CH chunks of features; CHAIN: one at a time, in the last step's stage
+    constexpr int CH = CHAIN && C::CH > 8 ? 8 : C::CH, SLICES = C::CH / CH, TMS = TM / SLICES;
+    static_assert(!CHAIN || C::GWAVES * 32 * CH * 16 <= C::STAGE, "the slices fit a stage");
+    uint8_t* region = CHAIN ? lds_all + (st_end == 0 ? (NSTAGE - 1) * C::STAGE : st_end - C::STAGE) + wave * (32 * CH * 16)
+                            : lds_all + (count + wave / C::RPS) % NSTAGE * C::STAGE + wave % C::RPS * C::REGION;
     const int m_wave = m0 + wm * C::WTM, n_wave = n0 + wn * C::WTN;
-    const int m = m_wave + 8 * (lane % C::CH), left = args.M - m;     // a lane's features of a whole row
-    constexpr int TPP = 64 / C::CH, PASSES = 32 / TPP;                  // tokens a pass, passes a slice
+    constexpr int TPP = 64 / CH, PASSES = 32 / TPP;                     // tokens a pass, passes a slice
     // Rows of whole cache lines stream past the L2, which would only flush them
     // (8192^3 277 -> 263 us, 2304 x 768 with 4096 tokens 13.0 -> 10.7); parts of
     // lines are joined there (7023 x 192 with 5744 tokens 36 us, 49 streamed).
     const __amdgpu_buffer_rsrc_t y_rsrc =
         f8_rsrc((const uint8_t*)args.Y + ((int64_t)n_wave * args.ldy + m_wave) * 2, 0xFFFFFFFFu);
     // a lane's 16 B of the region's token t
-    auto chunk = [&](int t) { return region + t * (C::CH * 16) + ((lane % C::CH) ^ (t % C::CH)) * 16; };
+    auto chunk = [&](int t) { return region + t * (CH * 16) + ((lane % CH) ^ (t % CH)) * 16; };
     if (!GROUPED && args.residual && !residual_dma) {
       // rows at any alignment come through registers, four passes at a time
+      const int m = m_wave + 8 * (lane % CH), left = args.M - m;
 #pragma unroll 1
       for (int t0 = r_t; t0 < C::WTN; t0 += 4 * TPP) {
         u32x4 r[4];
@@ -566,58 +672,63 @@ __device__ __forceinline__ void f8_block_tile(const F8Args& args, uint8_t* lds_a
     for (int j = 0; j < TN; ++j) {
       const float sx = sc[2 * BM + wn * C::WTN + 32 * j + nl];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        float z[16];
+      for (int slice = 0; slice < SLICES; ++slice) {
+        const int m = m_wave + 8 * (CH * slice + lane % CH), left = args.M - m;     // a lane's features of a whole row
+        const int t_first = CHAIN ? 0 : 32 * j;                                     // in the region
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int f = wm * C::WTM + 32 * i + 8 * q + 4 * h;
-          const f32x4 w = *reinterpret_cast<const f32x4*>(sc + f);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) z[4 * q + u] = acc[i][j][4 * q + u] * sx * w[u];   // sx w alone can leave fp32
-        }
-        if (args.bias) {
+        for (int i = slice * TMS; i < (slice + 1) * TMS; ++i) {
+          float z[16];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const f32x4 b4 = *reinterpret_cast<const f32x4*>(sc + BM + wm * C::WTM + 32 * i + 8 * q + 4 * h);
+            const int f = wm * C::WTM + 32 * i + 8 * q + 4 * h;
+            const f32x4 w = *reinterpret_cast<const f32x4*>(sc + f);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) z[4 * q + u] += b4[u];
+            for (int u = 0; u < 4; ++u) z[4 * q + u] = acc[i][j][4 * q + u] * sx * w[u];   // sx w alone can leave fp32
           }
-        }
-        f8_act<sizeof(OutT) == 4>(z, args.act);
-        uint8_t* place[4];
+          if (args.bias) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          place[q] = region + (32 * j + nl) * (C::CH * 16) + (((4 * i + q) ^ (nl % C::CH)) * 16) + 8 * h;
-        if (args.residual) {
+            for (int q = 0; q < 4; ++q) {
+              const f32x4 b4 = *reinterpret_cast<const f32x4*>(sc + BM + wm * C::WTM + 32 * i + 8 * q + 4 * h);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const u32x2 r = *reinterpret_cast<const u32x2*>(place[q]);
-            z[4 * q] += bf16_lo(r[0]);
-            z[4 * q + 1] += bf16_hi(r[0]);
-            z[4 * q + 2] += bf16_lo(r[1]);
-            z[4 * q + 3] += bf16_hi(r[1]);
+              for (int u = 0; u < 4; ++u) z[4 * q + u] += b4[u];
+            }
           }
+          f8_act<sizeof(OutT) == 4>(z, args.act);
+          uint8_t* place[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            place[q] = region + (t_first + nl) * (CH * 16) + (((4 * (i - slice * TMS) + q) ^ (nl % CH)) * 16) + 8 * h;
+          if (args.residual) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const u32x2 r = *reinterpret_cast<const u32x2*>(place[q]);
+              z[4 * q] += bf16_lo(r[0]);
+              z[4 * q + 1] += bf16_hi(r[0]);
+              z[4 * q + 2] += bf16_lo(r[1]);
+              z[4 * q + 3] += bf16_hi(r[1]);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<u32x2*>(place[q]) =
+                (u32x2){pack_bf16(z[4 * q], z[4 * q + 1]), pack_bf16(z[4 * q + 2], z[4 * q + 3])};
         }
+        u32x4 v[PASSES];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<u32x2*>(place[q]) =
-              (u32x2){pack_bf16(z[4 * q], z[4 * q + 1]), pack_bf16(z[4 * q + 2], z[4 * q + 3])};
-      }
-      u32x4 v[PASSES];
+        for (int t = 0; t < PASSES; ++t) v[t] = *reinterpret_cast<const u32x4*>(chunk(t_first + t * TPP + lane / CH));
 #pragma unroll
-      for (int t = 0; t < PASSES; ++t) v[t] = *reinterpret_cast<const u32x4*>(chunk(32 * j + t * TPP + r_t));
+        for (int t = 0; t < PASSES; ++t) {
+          const int token = 32 * j + t * TPP + lane / CH, n = n_wave + token;
+          if (n >= args.N) continue;
+          uint16_t* p = (uint16_t*)args.Y + (int64_t)n * args.ldy + m;
+          if (left >= 8) {
+            if (args.stream) stream_16b(y_rsrc, v[t], (uint32_t)(token * args.ldy + 8 * (CH * slice + lane % CH)) * 2);
+            else *reinterpret_cast<u32x4_a2*>(p) = v[t];
+          } else {
 #pragma unroll
-      for (int t = 0; t < PASSES; ++t) {
-        const int n = n_wave + 32 * j + t * TPP + r_t;
-        if (n >= args.N) continue;
-        uint16_t* p = (uint16_t*)args.Y + (int64_t)n * args.ldy + m;
-        if (left >= 8) {
-          if (args.stream) stream_16b(y_rsrc, v[t], (uint32_t)((32 * j + t * TPP + r_t) * args.ldy + 8 * (lane % C::CH)) * 2);
-          else *reinterpret_cast<u32x4_a2*>(p) = v[t];
-        } else {
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (u < left) p[u] = (uint16_t)(v[t][u / 2] >> (16 * (u & 1)));
+            for (int u = 0; u < 8; ++u)
+              if (u < left) p[u] = (uint16_t)(v[t][u / 2] >> (16 * (u & 1)));
+          }
         }
       }
     }

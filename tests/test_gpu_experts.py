@@ -7,6 +7,7 @@ from the largest is rounded once (at most |l - max| U of exp's argument), exp an
 8 U, a sum of E terms E U.
 Grouped product: as for the product it is made of (test_gpu_f8).
 Combination: k products summed in fp32 and the residual: (k + 2) U of the sum of magnitudes."""
+import gc
 import math
 
 import numpy as np
@@ -18,6 +19,14 @@ from gpu_util import need_gpu, torch
 p24 = pytest.importorskip("structured_sparse_gemm_prune24_amd")
 pytestmark = pytest.mark.gpu
 D = torch.float64
+
+
+@pytest.fixture
+def large_blocks():
+    """Blocks that a test leaves in the allocator's cache go back, before anything that lives on takes a part of one."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
 
 
 def _gen(seed):
@@ -263,6 +272,31 @@ def test_grouped_is_each_experts_product(monkeypatch, tile):
         at += m
 
 
+@pytest.mark.parametrize("K", [448, 576, 640, 832])
+@pytest.mark.parametrize("tile", [None, "128x128", "256x128", "256x192", "256x256"])
+def test_grouped_over_several_tiles_a_block(monkeypatch, large_blocks, tile, K):
+    """More tiles than the chip holds at once, of every fill, so that blocks go from one to the next; 4 to 7 steps of K,
+    the last one half where K is odd in 64s."""
+    need_gpu()
+    if tile:
+        monkeypatch.setenv("P24_F8_TILE", tile)
+    E, M = 90, 1100
+    counts = torch.randint(0, 601, (E,), generator=torch.Generator().manual_seed(K)).tolist()
+    counts[3] = counts[64] = 0
+    counts[10], counts[65], counts[89] = 1, 256, 257
+    n = sum(counts)
+    c = _weights(K, E, M, K)
+    x = _x(K + 1, n, K)
+    _check_grouped(c, x, counts)
+    bias = _randn(5, E, M)
+    few = _x(K + 2, 1001, K)
+    tokens = torch.randint(0, 1001, (n,), generator=_gen(K), device="cuda", dtype=torch.int32)
+    _check_grouped(c, few, counts, tokens=tokens, bias=bias, name="silu")
+    y = p24.spmm24_f8_grouped(c, x, _offsets(counts))
+    for _ in range(3):
+        assert torch.equal(y, p24.spmm24_f8_grouped(c, x, _offsets(counts)))
+
+
 def test_grouped_offsets_and_tokens_outside():
     """Offsets past the rows and tokens outside X reach nothing outside: what they do reach is defined."""
     need_gpu()
@@ -431,7 +465,7 @@ def test_route_of_scores_that_32_bits_cannot_tell_apart(T):
         _check_route(l, k, score="sigmoid", bias=bias - 1000.0)     # the bias swallows the sigmoid's last bits in 32
 
 
-def test_offsets_past_32_bits():
+def test_offsets_past_32_bits(large_blocks):
     """Outputs and combined rows of more than 2^31 elements: the last rows are those of a small call."""
     need_gpu()
     M, n = 32768, 70000
