@@ -7,8 +7,8 @@
 // every group adds up the counts ahead of it (from the L2: T / 32 x E) and places
 // its rows.  Past 8192 tokens a launch between them sums the counts once for all;
 // up to 64 tokens one launch does everything.
-// Bound by instructions: about 90 for each choice of four tokens.  8192 tokens, 8 of 256 experts with a bias: 18.5 us,
-// 10 to pick and 8 to place; one token, 8 of 128: 5.5, a launch.
+// Bound by instructions: about 90 for each choice of four tokens.  8192 tokens, 8 of 256 experts with a bias: 16 us,
+// 10 to pick and 6 to place; one token, 8 of 128: 5.5, a launch.
 //
 // Combination: bound by HBM, T (k + 2) rows.  4096 tokens of 8 rows of 4096 bf16: 65 us, 5.1 TB/s.
 #include <type_traits>
@@ -249,14 +249,15 @@ constexpr int GROUP = 32;       // tokens whose choices are counted together
 constexpr int FEW = 64;         // tokens that one block takes
 constexpr int SLOTS = P24_EXPERTS_MAX;
 
-// base[e] = rows of lower experts + ahead[e], from the experts' rows total[e] (LDS); the sums alone to `offsets`, if
+// base[e] = rows of lower experts + ahead(e), from the experts' rows total(e); the sums alone to `offsets`, if
 // given.  All threads of the block.  Returns the number of rows in all.
-__device__ __forceinline__ int scan_experts(int* base, const int* total, const int* ahead, int E, int* offsets) {
+template <typename Total, typename Ahead>
+__device__ __forceinline__ int scan_experts(int* base, Total total, Ahead ahead, int E, int* offsets) {
   __shared__ int waves[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, count = blockDim.x >> 6;
   int carry = 0;
   for (int e0 = 0; e0 < E; e0 += blockDim.x) {
-    const int e = e0 + threadIdx.x, mine = e < E ? total[e] : 0;
+    const int e = e0 + threadIdx.x, mine = e < E ? total(e) : 0;
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -271,7 +272,7 @@ __device__ __forceinline__ int scan_experts(int* base, const int* total, const i
       sum += waves[w];
     }
     if (e < E) {
-      base[e] = before + upto - mine + (ahead ? ahead[e] : 0);
+      base[e] = before + upto - mine + ahead(e);
       if (offsets) offsets[e] = before + upto - mine;
     }
     carry += sum;
@@ -322,6 +323,10 @@ __device__ __forceinline__ void pick_group(const RouteArgs& a, int t0, Word* cho
   }
 }
 
+// Up to MOST_ADDED groups every block adds up their counts itself; a group's lie in one byte each then, rows of whole words.
+constexpr int MOST_ADDED = 256;
+__device__ __forceinline__ int count_words(int E) { return (E + 3) / 4; }
+
 // 32 tokens a block: picks, and counts the rows.
 template <typename T, bool BIAS, int V>
 __global__ __launch_bounds__(512) void k_route_pick(const RouteArgs a) {
@@ -330,21 +335,28 @@ __global__ __launch_bounds__(512) void k_route_pick(const RouteArgs a) {
   __syncthreads();
   pick_group<T, BIAS, V>(a, blockIdx.x * GROUP, chosen);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = __popc(chosen[e]);
+  if (gridDim.x > MOST_ADDED) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = __popc(chosen[e]);
+    return;
+  }
+  for (int w = threadIdx.x; w < count_words(a.E); w += blockDim.x) {
+    unsigned c = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) c |= 4 * w + u < a.E ? __popc(chosen[4 * w + u]) << (8 * u) : 0;
+    reinterpret_cast<unsigned*>(a.counts)[(int64_t)blockIdx.x * count_words(a.E) + w] = c;
+  }
 }
 
 // 64 tokens at most, in one block.
 template <typename T, bool BIAS, int V>
 __global__ __launch_bounds__(512) void k_route_few(const RouteArgs a) {
   __shared__ unsigned long long chosen[SLOTS];
-  __shared__ int base[SLOTS], total[SLOTS], experts[FEW * P24_EXPERTS_K_MAX];
+  __shared__ int base[SLOTS], experts[FEW * P24_EXPERTS_K_MAX];
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) chosen[e] = 0;
   __syncthreads();
   pick_group<T, BIAS, V>(a, 0, chosen, experts);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) total[e] = __popcll(chosen[e]);
-  __syncthreads();
-  const int rows = scan_experts(base, total, nullptr, a.E, a.offsets);
+  const int rows = scan_experts(base, [&](int e) { return __popcll(chosen[e]); }, [](int) { return 0; }, a.E, a.offsets);
   place_rows(a, 0, experts, chosen, base);
   no_tokens(a, rows, threadIdx.x, blockDim.x);
 }
@@ -381,13 +393,19 @@ __global__ __launch_bounds__(1024) void k_route_sum(const RouteArgs a, int group
 template <bool SUMMED>
 __global__ __launch_bounds__(1024) void k_route_place(const RouteArgs a) {
   __shared__ unsigned chosen[SLOTS];
-  __shared__ int base[SLOTS], total[SLOTS], ahead[SLOTS];
-  const int t0 = blockIdx.x * GROUP, groups = gridDim.x, E = a.E;
+  __shared__ int base[SLOTS];
+  __shared__ unsigned all[2][SLOTS / 4], lower[2][SLOTS / 4];
+  __shared__ int total[SUMMED ? SLOTS : 1], ahead[SUMMED ? SLOTS : 1];
+  const int t0 = blockIdx.x * GROUP, groups = gridDim.x, E = a.E, words = count_words(E);
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     chosen[e] = 0;
-    total[e] = SUMMED ? a.counts[(int64_t)groups * E + e] : 0;
-    ahead[e] = SUMMED ? a.counts[(int64_t)blockIdx.x * E + e] : 0;
+    if constexpr (SUMMED) {
+      total[e] = a.counts[(int64_t)groups * E + e];
+      ahead[e] = a.counts[(int64_t)blockIdx.x * E + e];
+    }
   }
+  if constexpr (!SUMMED)
+    for (int w = threadIdx.x; w < words; w += blockDim.x) all[0][w] = all[1][w] = lower[0][w] = lower[1][w] = 0;
   __syncthreads();
   const int n = min(a.T - t0, GROUP) * a.k;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -395,23 +413,33 @@ __global__ __launch_bounds__(1024) void k_route_place(const RouteArgs a) {
     if (e >= 0) atomicOr(&chosen[e], 1u << (i / a.k));
   }
   if constexpr (!SUMMED) {
-    // the groups' counts, several runs of groups side by side; the parts meet in LDS (whole numbers: any order)
-    const int width = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : E <= 512 ? 512 : 1024;
-    const int parts = 1024 / width, part = threadIdx.x / width, e = threadIdx.x % width;
-    if (e < E) {
-      int sum = 0, before = 0;
+    // the groups' counts, four experts a word, several runs of groups side by side; two sums of 16 bits a word (8192 tokens
+    // at most), whose parts meet in LDS (whole numbers: any order)
+    const int width = words <= 16 ? 16 : words <= 32 ? 32 : words <= 64 ? 64 : words <= 128 ? 128 : 256;
+    const int parts = 1024 / width, part = threadIdx.x / width, w = threadIdx.x % width;
+    if (w < words && part < groups) {
+      const unsigned* const col = reinterpret_cast<const unsigned*>(a.counts) + w;
+      unsigned sum[2] = {0, 0}, before[2] = {0, 0};
 #pragma unroll 8
       for (int g = part; g < groups; g += parts) {
-        const int c = a.counts[(int64_t)g * E + e];
-        sum += c;
-        before += g < (int)blockIdx.x ? c : 0;
+        const unsigned c = col[g * words], even = c & 0x00FF00FF, odd = (c >> 8) & 0x00FF00FF;
+        sum[0] += even;
+        sum[1] += odd;
+        before[0] += g < (int)blockIdx.x ? even : 0;
+        before[1] += g < (int)blockIdx.x ? odd : 0;
       }
-      atomicAdd(&total[e], sum);
-      atomicAdd(&ahead[e], before);
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        atomicAdd(&all[o][w], sum[o]);
+        atomicAdd(&lower[o][w], before[o]);
+      }
     }
   }
   __syncthreads();
-  const int rows = scan_experts(base, total, ahead, E, blockIdx.x == 0 ? a.offsets : nullptr);
+  const int rows = scan_experts(
+      base, [&](int e) { return SUMMED ? total[e] : (int)(all[e & 1][e / 4] >> (8 * (e & 2)) & 0xFFFF); },
+      [&](int e) { return SUMMED ? ahead[e] : (int)(lower[e & 1][e / 4] >> (8 * (e & 2)) & 0xFFFF); }, E,
+      blockIdx.x == 0 ? a.offsets : nullptr);
   place_rows(a, t0, a.experts + (int64_t)t0 * a.k, chosen, base);
   no_tokens(a, rows, blockIdx.x * 1024 + threadIdx.x, groups * 1024);
 }
@@ -428,7 +456,7 @@ static p24_status launch_route(const RouteArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((k_route_pick<T, BIAS, V>), dim3(groups), dim3(512), 0, st, a);
   p24_status s = launch_status();
   if (s != P24_OK) return s;
-  if (groups <= 256) {
+  if (groups <= MOST_ADDED) {
     hipLaunchKernelGGL(k_route_place<false>, dim3(groups), dim3(1024), 0, st, a);
     return launch_status();
   }
