@@ -5,7 +5,7 @@
 // is one word, whose bits count the expert's rows and rank them in token order.
 // The first launch picks and leaves the counts of each 32 tokens; in the second
 // every group adds up the counts ahead of it (from the L2: T / 32 x E) and places
-// its rows.  Past 8192 tokens a launch between them sums the counts once for all;
+// its rows.  Past 16384 tokens (of 256 experts) a launch between them sums the counts once for all;
 // up to 64 tokens one launch does everything.
 // Bound by instructions: about 90 for each choice of four tokens.  8192 tokens, 8 of 256 experts with a bias: 16 us,
 // 10 to pick and 6 to place; one token, 8 of 128: 5.5, a launch.
@@ -32,6 +32,7 @@ struct RouteArgs {
   int T, E, k;
   int score, normalize;
   float scale;
+  bool added;       // k_route_place sums the counts
 };
 
 // Keys whose unsigned order is the order of the scores: NaN above +inf, -0 as +0.  No score has key 0.
@@ -323,9 +324,13 @@ __device__ __forceinline__ void pick_group(const RouteArgs& a, int t0, Word* cho
   }
 }
 
-// Up to MOST_ADDED groups every block adds up their counts itself; a group's lie in one byte each then, rows of whole words.
-constexpr int MOST_ADDED = 256;
-__device__ __forceinline__ int count_words(int E) { return (E + 3) / 4; }
+// ADDED: every block adds up all groups' counts itself; a group's lie in one byte each then, rows of whole words.  That is groups^2
+// words from the L2, for a launch less: 16384 tokens of 256 experts 22.0 us, 24.1 with the launch (64 experts 13.0, 18.0), of
+// 1024 experts 69, 57.  The sums have 16 bits.
+__host__ __device__ __forceinline__ int count_words(int E) { return (E + 3) / 4; }
+static bool route_adds(int64_t groups, int E) {
+  return groups * GROUP < 65536 && groups * groups * count_words(E) <= 1 << 24;
+}
 
 // 32 tokens a block: picks, and counts the rows.
 template <typename T, bool BIAS, int V>
@@ -335,7 +340,7 @@ __global__ __launch_bounds__(512) void k_route_pick(const RouteArgs a) {
   __syncthreads();
   pick_group<T, BIAS, V>(a, blockIdx.x * GROUP, chosen);
   __syncthreads();
-  if (gridDim.x > MOST_ADDED) {
+  if (!a.added) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = __popc(chosen[e]);
     return;
   }
@@ -413,8 +418,8 @@ __global__ __launch_bounds__(1024) void k_route_place(const RouteArgs a) {
     if (e >= 0) atomicOr(&chosen[e], 1u << (i / a.k));
   }
   if constexpr (!SUMMED) {
-    // the groups' counts, four experts a word, several runs of groups side by side; two sums of 16 bits a word (8192 tokens
-    // at most), whose parts meet in LDS (whole numbers: any order)
+    // the groups' counts, four experts a word, several runs of groups side by side; two sums of 16 bits a word,
+    // whose parts meet in LDS (whole numbers: any order)
     const int width = words <= 16 ? 16 : words <= 32 ? 32 : words <= 64 ? 64 : words <= 128 ? 128 : 256;
     const int parts = 1024 / width, part = threadIdx.x / width, w = threadIdx.x % width;
     if (w < words && part < groups) {
@@ -447,16 +452,17 @@ __global__ __launch_bounds__(1024) void k_route_place(const RouteArgs a) {
 static int64_t route_groups(int64_t T) { return (T + GROUP - 1) / GROUP; }
 
 template <typename T, bool BIAS, int V>
-static p24_status launch_route(const RouteArgs& a, hipStream_t st) {
+static p24_status launch_route(RouteArgs a, hipStream_t st) {
   if (a.T <= FEW) {
     hipLaunchKernelGGL((k_route_few<T, BIAS, V>), dim3(1), dim3(a.T <= 16 ? 256 : 512), 0, st, a);
     return launch_status();
   }
   const unsigned groups = (unsigned)route_groups(a.T);
+  a.added = route_adds(groups, a.E);
   hipLaunchKernelGGL((k_route_pick<T, BIAS, V>), dim3(groups), dim3(512), 0, st, a);
   p24_status s = launch_status();
   if (s != P24_OK) return s;
-  if (groups <= MOST_ADDED) {
+  if (a.added) {
     hipLaunchKernelGGL(k_route_place<false>, dim3(groups), dim3(1024), 0, st, a);
     return launch_status();
   }

@@ -171,6 +171,26 @@ def test_route_of_one_expert_for_all():
     assert torch.equal(r.tokens, torch.arange(700, device="cuda", dtype=torch.int32))
 
 
+@pytest.mark.parametrize("T,E,k", [(16384, 256, 8), (16385, 256, 1), (32768, 64, 2), (32800, 62, 2), (65504, 3, 1), (65505, 3, 1), (8192, 1021, 4),
+                                   (70000, 5, 5)])
+def test_route_of_many_tokens(T, E, k):
+    """On both sides of where the counts are summed by a launch of their own; every token on one expert as well, the most a sum holds."""
+    need_gpu()
+    l = _randn(T + E, T, E)
+    for logits in (l, torch.arange(E, 0, -1, device="cuda", dtype=torch.float32).repeat(T, 1)):
+        r = p24.route(logits, k)
+        chosen = r.experts.long()
+        want = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :k]
+        assert torch.equal(chosen, want)
+        order = torch.sort(chosen.flatten(), stable=True).indices
+        assert torch.equal(r.tokens.long(), order // k)
+        at = torch.empty_like(order)
+        at[order] = torch.arange(T * k, device="cuda")
+        assert torch.equal(r.positions.long().flatten(), at)
+        count = torch.bincount(chosen.flatten(), minlength=E)
+        assert torch.equal(r.offsets.long(), torch.cat([count.new_zeros(1), count.cumsum(0)]))
+
+
 def test_route_without_tokens():
     need_gpu()
     r = p24.route(torch.empty(0, 9, device="cuda"), 3)
