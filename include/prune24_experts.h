@@ -42,8 +42,11 @@ enum { P24_SCORE_SOFTMAX = 0, P24_SCORE_SIGMOID = 1 };
  *   normalize softmax: weights exp(l - max) over their sum, of the chosen experts
  *             (1) or of all (0).  sigmoid: the sigmoids (without the bias), over
  *             their sum (1) or as they are (0).  Then times `scale` (finite).
- *             Computed in fp32.  A NaN logit, or +inf under softmax, gives the NaN
- *             that the formula gives.
+ *             Computed in fp32; quotients of sigmoids that leave it are those of
+ *             the sigmoids themselves.  A NaN logit, or +inf under softmax, gives
+ *             the NaN that the formula gives, and so do normalized sigmoids whose
+ *             largest logit lies below -709.78, 0 / 0 in 64 bits too (the lowest
+ *             value of a type is no mask for them: -inf is).
  *   experts   T x k int32: the chosen experts, best first; -1 past the open ones.
  *   weights   T x k fp32; 0 where there is no expert.
  *   offsets   E + 1 int32: expert e's rows are [offsets[e], offsets[e + 1]).

@@ -242,6 +242,17 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int (&exp
       if (expert[s] >= 0) w[s] = 1.0f / (1.0f + expf(-at[s]));
   }
   if (a.normalize) all = sum_of(w[0] + w[1]);
+  // Sigmoids leave fp32 where their quotients do not: all of them 0 below -88.7.  With a sum this small all logits l lie
+  // below -2, and exp(l - max) / (1 + exp(l)) are the sigmoids over exp(max), none of which counts and is lost.
+  // (Below -709.78 exp(-l) leaves 64 bits too: there the formula's quotient is 0 / 0.)
+  if (a.normalize && a.score == P24_SCORE_SIGMOID && all < 0.119f) {
+    const float low = fmaxf(expert[0] >= 0 ? at[0] : -INFINITY, expert[1] >= 0 ? at[1] : -INFINITY);
+    const float most = key_score(max_of(score_key(low)));
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (expert[s] >= 0) w[s] = most > -709.78271f ? expf(at[s] - most) / (1.0f + expf(at[s])) : 0.0f;
+    all = sum_of(w[0] + w[1]);
+  }
 #pragma unroll
   for (int s = 0; s < 2; ++s) weight[s] = expert[s] >= 0 ? w[s] / all * a.scale : 0.0f;
 }
