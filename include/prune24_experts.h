@@ -76,7 +76,8 @@ P24_API p24_status experts_route(const void* logits, int32_t l_dtype, int64_t ld
  *   X         x_rows x K e4m3, leading dimension ldx, as for spmm24_f8; with
  *             `tokens` x_rows * ldx < 2^32.  Without it x_rows is `rows`.
  *   offsets   E + 1 int32 on the device, not falling, offsets[0] >= 0.  Offsets past
- *             `rows` are taken as `rows`: nothing is read or written outside.
+ *             `rows` are taken as `rows`: nothing is read or written outside.  Where
+ *             they fall, which rows are written is not said, but none outside Y.
  *   tokens    rows int32, or NULL.  A value outside [0, x_rows) in an expert's
  *             range reads the last row of X.
  *   Y         rows x M as for spmm24_f8.  Rows outside every expert's range, those

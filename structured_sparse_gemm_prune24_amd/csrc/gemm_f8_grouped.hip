@@ -63,25 +63,14 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8_grouped(const F
   uint8_t lds[f8_lds_bytes<BM, BN, WGM, WGN, LW, KG, OutT>() + (CHAIN ? F8Chain<C>::TOKENS : 0)];
   F8GroupSearch<BN> search(g.groups);
   const uint32_t nbm = g.a.nbm, tiles = search.total() * nbm;
-  struct Tile {
-    int expert, first, count;
-    uint32_t bm, bn;
-  };
-  auto find = [&](uint32_t i, Tile& t) {
-    const uint32_t b = xcd_remap(i, tiles);
-    uint32_t first_tile;
-    if (!search.find(b / nbm, t.expert, t.first, t.count, first_tile)) return false;   // (never: b < tiles)
-    f8_place(b - first_tile * nbm, nbm, F8GroupSearch<BN>::tiles_of(t.count), t.bm, t.bn);
-    return true;
-  };
   F8Chain<C> chain;
-  Tile tile;
+  F8GroupTile tile;
   uint32_t i = blockIdx.x;
-  if (i >= tiles || !find(i, tile)) return;
+  if (i >= tiles || !search.tile(i, tiles, nbm, tile)) return;
   for (;;) {
     i += gridDim.x;
-    Tile next = tile;
-    const bool more = i < tiles && find(i, next);
+    F8GroupTile next = tile;
+    const bool more = i < tiles && search.tile(i, tiles, nbm, next);
     F8RowMap rows;
     const F8Args a = f8_part<OutT>(g, tile.expert, tile.first, tile.count, rows);
     if constexpr (CHAIN) {
@@ -105,12 +94,7 @@ __global__ __launch_bounds__(WGM * WGN * KG * 64) void k_gemm_f8_grouped(const F
   }
 }
 
-// Most tiles of BN rows that `rows` rows of E experts can take: every expert with rows has one part tile at most.
-static int64_t f8_most_tiles(const F8GroupedArgs& g, int bn) {
-  const int64_t live = g.groups.experts < g.groups.rows ? g.groups.experts : g.groups.rows;
-  const int64_t most = (g.groups.rows - live) / bn + live;
-  return most;
-}
+static int64_t f8_most_tiles(const F8GroupedArgs& g, int bn) { return f8_most_tiles(g.groups.rows, g.groups.experts, bn); }
 
 template <int W, typename OutT>
 static p24_status launch_tokens_grouped(const F8GroupedArgs& g, hipStream_t st) {

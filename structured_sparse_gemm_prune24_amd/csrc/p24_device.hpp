@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "p24_places.hpp"
+
 namespace p24 {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -75,18 +77,6 @@ __device__ __forceinline__ uint32_t compress_group(const uint32_t b[4], uint16_t
   v0 = GroupIO<T>::to_bf16(w0);
   v1 = GroupIO<T>::to_bf16(w1);
   return code;
-}
-
-// XCD-aware block order.  Workgroups are handed to the 8 XCDs round-robin, so
-// block b runs on XCD b % 8.  Renumbering so that each XCD receives one
-// contiguous range of logical tiles keeps neighbouring tiles (which share rows
-// of W and columns of X) in the same XCD's L2.
-__device__ __forceinline__ uint32_t xcd_remap(uint32_t b, uint32_t nblocks) {
-  constexpr uint32_t NXCD = 8;
-  const uint32_t per = nblocks / NXCD;          // full rounds
-  const uint32_t full = per * NXCD;
-  if (b >= full) return b;                      // the ragged last round keeps its ids
-  return (b % NXCD) * per + (b / NXCD);
 }
 
 }  // namespace p24

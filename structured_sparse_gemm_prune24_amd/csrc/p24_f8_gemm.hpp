@@ -245,16 +245,6 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Row block and token tile of block b of nbm x nbn: groups of eight row blocks.
-__device__ __forceinline__ void f8_place(uint32_t b, uint32_t nbm, uint32_t nbn, uint32_t& bm, uint32_t& bn) {
-  constexpr uint32_t GROUP = 8;
-  const uint32_t group_size = GROUP * nbn;
-  const uint32_t first_m = (b / group_size) * GROUP;
-  const uint32_t gsz = min(nbm - first_m, GROUP);
-  bm = first_m + (b % group_size) % gsz;
-  bn = (b % group_size) / gsz;
-}
-
 template <int BM, int BN, int WGM, int WGN, int LW, int KG, typename OutT>
 constexpr int f8_lds_bytes() {
   using C = F8Tile<BM, BN, WGM, WGN, LW, KG>;

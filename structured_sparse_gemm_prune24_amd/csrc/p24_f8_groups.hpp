@@ -2,10 +2,14 @@
 //
 // `offsets` lies on the device: the launch knows an upper bound of the tiles only, and each block finds
 // its own.  Lane l of a wave holds expert 64 chunk + l's range; an inclusive sum over the lanes gives
-// the tiles up to it.  Ranges are clipped to [0, rows], so that no offset leads outside the output.
+// the tiles up to it.  Ranges are clipped to [0, rows], so that no offset leads outside the output, and offsets
+// that fall have no tiles: their ranges could overlap, and the tiles be more than the launch and the walk allow for.
 #pragma once
 
+#include "p24_places.hpp"
+#ifdef __HIP__
 #include "p24_device.hpp"
+#endif
 
 namespace p24 {
 
@@ -14,6 +18,18 @@ struct F8Groups {
   const int* tokens;    // row of X of each row of Y, or nullptr: the same row
   int experts, rows;    // rows of Y
   int x_rows;           // rows of X
+};
+
+// Most tiles of bn rows that `rows` rows of `experts` experts can take: every expert with rows has one part tile at most.
+P24_HD int64_t f8_most_tiles(int64_t rows, int64_t experts, int bn) {
+  const int64_t live = experts < rows ? experts : rows;
+  return (rows - live) / bn + live;
+}
+
+// A tile: row block bm and rows bn BN on of an expert's `count` rows from `first` on.
+struct F8GroupTile {
+  int expert, first, count;
+  uint32_t bm, bn;
 };
 
 template <int BN>
@@ -28,25 +44,28 @@ struct F8GroupSearch {
 
   __device__ __forceinline__ F8GroupSearch(const F8Groups& groups) : g(groups), lane(threadIdx.x & 63) {}
 
-  __device__ __forceinline__ void range(int c, int& first, int& count) const {
+  // false where the offsets fall
+  __device__ __forceinline__ bool range(int c, int& first, int& count) const {
     const int e = 64 * c + lane;
     const int a = e < g.experts ? g.offsets[e] : 0, b = e < g.experts ? g.offsets[e + 1] : 0;
     first = min(max(a, 0), g.rows);
-    count = max(min(b, g.rows) - first, 0);
+    count = max(min(b, g.rows), first) - first;      // (a difference of any two ints would wrap)
+    return a <= b;
   }
   static __device__ __forceinline__ uint32_t tiles_of(int rows) { return ((uint32_t)rows + BN - 1) / BN; }
 
-  // tiles of all experts
+  // tiles of all experts; 0 if the offsets fall
   __device__ __forceinline__ uint32_t total() const {
     uint32_t sum = 0;
+    bool rise = true;
     for (int c = 0; 64 * c < g.experts; ++c) {
       int first, count;
-      range(c, first, count);
+      rise &= range(c, first, count);
       sum += tiles_of(count);
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-    return __builtin_amdgcn_readfirstlane(sum);
+    return __ballot(!rise) ? 0 : __builtin_amdgcn_readfirstlane(sum);
   }
   // The expert of tile t, its first row and rows, and its first tile.  t does not fall from call to call;
   // false past the last tile.
@@ -69,6 +88,15 @@ struct F8GroupSearch {
     first = __builtin_amdgcn_readlane(lo, l);
     count = __builtin_amdgcn_readlane(n, l);
     first_tile = before + __builtin_amdgcn_readlane(upto, l) - tiles_of(count);
+    return true;
+  }
+  // Tile i of `tiles`, total() times the nbm row blocks.  A block asks for i, i + grid, ...: the grid is a multiple of the
+  // XCDs' number or holds all tiles, so that xcd_remap's numbers do not fall.
+  __device__ __forceinline__ bool tile(uint32_t i, uint32_t tiles, uint32_t nbm, F8GroupTile& t) {
+    const uint32_t b = xcd_remap(i, tiles);
+    uint32_t first_tile;
+    if (!find(b / nbm, t.expert, t.first, t.count, first_tile)) return false;   // (never: b < tiles)
+    f8_place(b - first_tile * nbm, nbm, tiles_of(t.count), t.bm, t.bn);
     return true;
   }
 };

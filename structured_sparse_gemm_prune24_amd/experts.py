@@ -132,8 +132,8 @@ def spmm24_f8_grouped(c: Experts24F8, X: Quantized8, offsets, tokens=None, out_d
                       act="none"):
     """Y[p] = act(W[e] X[tokens[p]] + bias[e]) for the rows p of each expert e, offsets[e] to offsets[e + 1].
 
-    X.values [rows of X, K] e4m3 (rows 16-byte aligned), X.scale fp32; offsets int32 [E + 1]; tokens
-    int32 [rows]: which row of X a row takes, or None: row p itself; bias fp32 [E, M].  Y has one row for
+    X.values [rows of X, K] e4m3 (rows 16-byte aligned), X.scale fp32; offsets int32 [E + 1], not
+    falling; tokens int32 [rows]: which row of X a row takes, or None: row p itself; bias fp32 [E, M].  Y has one row for
     each entry of `tokens` (of X without).  Rows behind the last expert's are not written: they keep what
     `out` held."""
     v = X.values

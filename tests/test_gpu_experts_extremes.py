@@ -1,4 +1,5 @@
-"""GPU tests of the expert operators where their arguments leave the ordinary: sigmoids that leave fp32.
+"""GPU tests of the expert operators where their arguments leave the ordinary: sigmoids that leave fp32, offsets
+that fall.
 
 U = 2^-24 is half an fp32 step, relative."""
 import numpy as np
@@ -54,3 +55,32 @@ def test_sigmoids_that_leave_fp32_have_finite_quotients(T, E, k, dtype, with_bia
     n = p24.route(l, k, score="sigmoid", bias=bias, normalize=False)
     y = torch.sigmoid(l.to(D).gather(1, n.experts.long()))
     assert torch.all((n.weights.to(D) - y).abs() <= (x.abs() + 24) * U * y + 1e-37)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tile", [None, "tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x192", "256x256"])
+def test_falling_offsets_write_nothing_outside(monkeypatch, tile, out):
+    """Offsets that fall (no routing makes them) have no rows; the kernel for few rows may write some, none outside `out`.
+    The same call with sums of counts, afterwards, is right."""
+    need_gpu()
+    if tile:
+        monkeypatch.setenv("P24_F8_TILE", tile)
+    E, rows, M, K = 70, 300, 300, 192
+    one = p24.compress_f8(0.02 * _randn(1, M, K))
+    c = p24.Experts24F8(one.data.repeat(E), one.scale.repeat(E, 1), E, M, K)
+    x = p24.gated_act(_randn(2, rows, K), act="none")
+    full = torch.full((rows + 8, M), 7.0, dtype=out, device="cuda")
+    for offsets in ([0, 300] * 35 + [0], [300] * 35 + [0] * 36, [0] * 68 + [300, 0, 300], [(1 << 31) - 1, -(1 << 31)] * 35 + [0]):
+        p24.spmm24_f8_grouped(c, x, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=full[4:-4])
+        torch.cuda.synchronize()
+        assert (full[:4] == 7).all() and (full[-4:] == 7).all()
+        if tile not in (None, "tokens"):
+            assert (full == 7).all()
+    good = torch.tensor([0] * 30 + [200] * 30 + [300] * 11, dtype=torch.int32, device="cuda")
+    y = p24.spmm24_f8_grouped(c, x, good, out_dtype=out)
+    X, W = x.values.to(D) * x.scale.to(D)[:, None], p24.decompress_f8(one).to(D)
+    size = X.abs() @ W.abs().T
+    # as in test_gpu_experts: K + 16 roundings of the sum, the 8-bit unit's cut, and the output's own
+    err = ((K + 16) * U + (7 * 2.0 ** -13 if out == torch.bfloat16 else 0)) * size
+    want = X @ W.T
+    assert torch.all((y.to(D) - want).abs() <= err + (2.0 ** -8 if out == torch.bfloat16 else U) * (want.abs() + err) + 1e-36)
