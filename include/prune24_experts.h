@@ -83,7 +83,8 @@ P24_API p24_status experts_route(const void* logits, int32_t l_dtype, int64_t ld
  *   Y         rows x M as for spmm24_f8.  Rows outside every expert's range, those
  *             from offsets[E] on among them, are left as they were.
  *   bias      E x M fp32, or NULL.  act as for spmm24_f8.
- *   1 <= E <= P24_EXPERTS_MAX; rows, M and K as N, M and K of spmm24_f8.
+ *   1 <= E <= P24_EXPERTS_MAX; rows, M and K as N, M and K of spmm24_f8: at most
+ *   65535 * 32 rows (the T k of a routing), else P24_ERR_UNSUPPORTED.
  * Sums are those of spmm24_f8: exact products and fp32 sums for P24_F32 outputs,
  * the 8-bit matrix unit's for P24_BF16.  P24_F8_TILE forces a kernel, as there.
  */

@@ -99,7 +99,6 @@ static int64_t f8_most_tiles(const F8GroupedArgs& g, int bn) { return f8_most_ti
 template <int W, typename OutT>
 static p24_status launch_tokens_grouped(const F8GroupedArgs& g, hipStream_t st) {
   const dim3 grid((unsigned)((g.a.M + 31) / 32), (unsigned)f8_most_tiles(g, 32));
-  if (grid.y > 65535) return P24_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((k_f8_tokens_grouped<W, OutT>), grid, dim3(W * 64), 0, st, g);
   return launch_status();
 }
@@ -147,20 +146,22 @@ constexpr TileCost GROUPED_F32[G_256x192] = {
 };
 
 static F8GroupedKernel choose_grouped(const F8GroupedArgs& g, bool exact) {
+  // the kernel for few rows has a block for every tile that there could be: as many as a grid holds in y
+  const F8GroupedKernel first = f8_most_tiles(g, 32) <= 65535 ? G_TOKENS : G_64x32;
   if (const char* e = getenv("P24_F8_TILE")) {
     static const char* const names[G_KERNELS] = {"tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x192", "256x256"};
     for (int i = 0; i < G_KERNELS; ++i)
-      if (strcmp(e, names[i]) == 0) return exact && i > G_256x128 ? G_256x128 : (F8GroupedKernel)i;
+      if (strcmp(e, names[i]) == 0) return exact && i > G_256x128 ? G_256x128 : i < first ? first : (F8GroupedKernel)i;
   }
   const TileCost* costs = exact ? GROUPED_F32 : GROUPED_BF16;
   const double rows = g.groups.rows, experts = g.groups.experts;
   const double live = experts * -expm1(-rows / experts), mean = rows / live;    // experts with rows, theirs on average
-  int best = 0;
+  int best = first;
   double least = 0;
-  for (int i = 0; i < (exact ? G_256x192 : G_KERNELS); ++i) {
+  for (int i = first; i < (exact ? G_256x192 : G_KERNELS); ++i) {
     const TileCost& c = costs[i];
     const double us = c.us(live / -expm1(-c.bn / mean) * ((g.a.M + c.bm - 1) / c.bm), g.a.K);
-    if (i == 0 || us < least) {
+    if (i == first || us < least) {
       least = us;
       best = i;
     }

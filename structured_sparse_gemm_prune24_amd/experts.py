@@ -134,7 +134,7 @@ def spmm24_f8_grouped(c: Experts24F8, X: Quantized8, offsets, tokens=None, out_d
 
     X.values [rows of X, K] e4m3 (rows 16-byte aligned), X.scale fp32; offsets int32 [E + 1], not
     falling; tokens int32 [rows]: which row of X a row takes, or None: row p itself; bias fp32 [E, M].  Y has one row for
-    each entry of `tokens` (of X without).  Rows behind the last expert's are not written: they keep what
+    each entry of `tokens` (of X without), at most 65535 * 32.  Rows behind the last expert's are not written: they keep what
     `out` held."""
     v = X.values
     if out is None and out_dtype in _STREAM_TYPES and act in _ACTS_F8:
@@ -212,7 +212,8 @@ def feed_forward_f8_experts(xq: Quantized8, logits, k: int, w_gate_up: Experts24
     W_down (act(gate) * up) with gate and up the halves of W_gate_up xq, weighed and added to the residual.
 
     xq: 8-bit rows of the norm [tokens, width]; logits [tokens, E]; w_gate_up E of 2F x width, gate rows
-    first; w_down E of width x F.  The result has the residual's type, else out_dtype."""
+    first; w_down E of width x F.  The result has the residual's type, else out_dtype.  tokens * k is at most
+    65535 * 32, the products' rows."""
     if w_gate_up.E != w_down.E or w_gate_up.M % 2 or w_gate_up.M // 2 != w_down.K or w_down.M != w_gate_up.K:
         raise ValueError(f"W_gate_up is {(w_gate_up.E, w_gate_up.M, w_gate_up.K)}, W_down "
                          f"{(w_down.E, w_down.M, w_down.K)}: not E of 2F x width and width x F")

@@ -1,8 +1,9 @@
 """GPU tests of the expert operators where their arguments leave the ordinary: sigmoids that leave fp32, offsets
-that fall.
+that fall, the most rows.
 
 U = 2^-24 is half an fp32 step, relative."""
-import numpy as np
+import gc
+
 import pytest
 
 from f8_ref import U
@@ -84,3 +85,35 @@ def test_falling_offsets_write_nothing_outside(monkeypatch, tile, out):
     err = ((K + 16) * U + (7 * 2.0 ** -13 if out == torch.bfloat16 else 0)) * size
     want = X @ W.T
     assert torch.all((y.to(D) - want).abs() <= err + (2.0 ** -8 if out == torch.bfloat16 else U) * (want.abs() + err) + 1e-36)
+
+
+@pytest.fixture
+def large_blocks():
+    """Blocks that a test leaves in the allocator's cache go back."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("tile", [None, "tokens"])
+@pytest.mark.parametrize("E", [2, 1024])
+def test_grouped_of_the_most_rows(monkeypatch, large_blocks, E, tile):
+    """65535 * 32 rows through narrow weights, more tiles than the kernel for few rows has blocks.
+
+    Whole numbers and scales of powers of two: exact."""
+    need_gpu()
+    if tile:
+        monkeypatch.setenv("P24_F8_TILE", tile)
+    rows, M, K = 65535 * 32, 32, 64
+    W = torch.zeros(E, M, K, device="cuda")
+    W[:, :, ::2] = torch.randint(-4, 5, (E, M, K // 2), device="cuda").float()
+    W[:, :, 0] = 448                      # the rows' scale is 1
+    c = p24.compress_f8_experts(W)
+    assert (c.scale == 1).all()
+    q = torch.randint(-2, 3, (rows, K), device="cuda").float()
+    x = p24.Quantized8(q.to(torch.float8_e4m3fn), torch.ones(rows, device="cuda"))
+    ends = torch.sort(torch.randint(0, rows + 1, (E - 1,))).values.tolist()
+    y = p24.spmm24_f8_grouped(c, x, torch.tensor([0] + ends + [rows], dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
+    for e, (a, b) in enumerate(zip([0] + ends, ends + [rows])):
+        if b > a:
+            assert torch.equal(y[a:b], q[a:b] @ W[e].T), e
