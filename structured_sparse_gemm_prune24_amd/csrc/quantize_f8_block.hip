@@ -6,7 +6,7 @@
 // 2048 x 11264 with a gate 29 us, 4.0 TB/s.
 //
 // The quotient y / s is correctly rounded, so that a value's 8 bits follow from the formula alone:
-// with i = 1 / s rounded, q = y i is within a step of it and q + (y - q s) i, the remainder taken
+// with i = 1 / s rounded, q = y i is within a step of it and q - (q s - y) i, the remainder taken
 // exactly by an fma, is the rounded quotient (Markstein).  Three instructions a value.
 #include "../../include/prune24_f8_block.h"
 #include "p24_api_internal.hpp"
@@ -41,11 +41,14 @@ struct BlockScale {
   __device__ __forceinline__ explicit BlockScale(uint32_t top) {
     s = f8_scale(__uint_as_float(top));
     inverse = 1.0f / s;
-    finite = s == INFINITY ? 0.0f : s;    // then y - q s is y, and the quotient y * 0
+    finite = s == INFINITY ? 0.0f : s;    // then q s - y is -y, and the quotient y * 0
   }
-  __device__ __forceinline__ float quotient(float y) const {
-    const float q = y * inverse;
-    return fmaf(fmaf(-q, finite, y), inverse, q);
+  __device__ __forceinline__ void divide(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = v[i] * inverse;
+      v[i] = fmaf(-inverse, fmaf(q, finite, -v[i]), q);      // in this order -0 stays -0
+    }
   }
 };
 
@@ -95,8 +98,7 @@ __global__ __launch_bounds__(256) void k_quantize_block(const QuantArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, mag(v[u][i]));
     const BlockScale s(quant_max16(top));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] = s.quotient(v[u][i]);
+    s.divide(v[u]);
     const int c = (b0 + u) * 128 + 8 * lane;
     store_row<8>((f8_t*)out + c, a.width - c, v[u]);
     if (lane == 0) a.scale[(b0 + u) * a.lds + t] = s.s;
@@ -129,8 +131,7 @@ __global__ __launch_bounds__(256) void k_quantize_weight(const QuantArgs a) {
   for (int u = 0; u < 8; ++u) {
     const int r = r0 + 16 * u;
     if (r >= a.rows) break;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] = s.quotient(v[u][i]);
+    s.divide(v[u]);
     store_row<8>((f8_t*)(a.values + r * a.ldv) + c, a.width - c, v[u]);
   }
   if (threadIdx.x == 0) a.scale[(int64_t)blockIdx.y * a.blocks + blockIdx.x] = s.s;
