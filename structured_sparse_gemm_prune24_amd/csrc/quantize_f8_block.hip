@@ -7,7 +7,8 @@
 //
 // The quotient y / s is correctly rounded, so that a value's 8 bits follow from the formula alone:
 // with i = 1 / s rounded, q = y i is within a step of it and q - (q s - y) i, the remainder taken
-// exactly by an fma, is the rounded quotient (Markstein).  Three instructions a value.
+// exactly by an fma, is the rounded quotient (Markstein).  Three instructions a value.  The remainder is a number of fp32
+// while s is 2^-90 or more; below, both are taken 2^64 times.
 #include "../../include/prune24_f8_block.h"
 #include "p24_api_internal.hpp"
 #include "p24_f8.hpp"
@@ -37,13 +38,19 @@ __device__ __forceinline__ uint32_t quant_max16(uint32_t v) {
 }
 
 struct BlockScale {
-  float s, finite, inverse;
+  float s, lift, finite, inverse;
   __device__ __forceinline__ explicit BlockScale(uint32_t top) {
     s = f8_scale(__uint_as_float(top));
-    inverse = 1.0f / s;
-    finite = s == INFINITY ? 0.0f : s;    // then q s - y is -y, and the quotient y * 0
+    lift = s < 0x1p-90f ? 0x1p64f : 1.0f;    // below, remainders would end under the smallest subnormal
+    const float lifted = s * lift;
+    inverse = 1.0f / lifted;
+    finite = s == INFINITY ? 0.0f : lifted;    // then q s - y is -y, and the quotient y * 0
   }
   __device__ __forceinline__ void divide(float (&v)[8]) const {
+    if (lift != 1.0f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= lift;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float q = v[i] * inverse;
