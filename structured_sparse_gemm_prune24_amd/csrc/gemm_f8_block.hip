@@ -351,6 +351,9 @@ __device__ __forceinline__ void f8_block_scaled_tile(const F8BArgs& args, uint8_
   steps_of<0, TN>([&](auto J) { tie(fb[decltype(J)::value]); });
   tie(fa[0][0]);
   tie(fa[0][1]);
+  asm volatile("" : "+v"(sw));
+#pragma unroll
+  for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(sx[j]));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 
