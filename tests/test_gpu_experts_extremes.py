@@ -1,5 +1,5 @@
 """GPU tests of the expert operators where their arguments leave the ordinary: sigmoids that leave fp32, offsets
-that fall, the most rows.
+that fall, the most rows; and the grouped product's every kernel on whole numbers.
 
 U = 2^-24 is half an fp32 step, relative."""
 import gc
@@ -117,3 +117,47 @@ def test_grouped_of_the_most_rows(monkeypatch, large_blocks, E, tile):
     for e, (a, b) in enumerate(zip([0] + ends, ends + [rows])):
         if b > a:
             assert torch.equal(y[a:b], q[a:b] @ W[e].T), e
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tile", [None, "tokens", "64x32", "64x64", "128x64", "128x128", "256x128", "256x192", "256x256"])
+def test_grouped_is_exact_on_whole_numbers(monkeypatch, large_blocks, tile, out):
+    """Whole numbers with scales of powers of two, gathered and not, more tiles than the chip holds at once and 7 steps of K
+    (blocks of the widest bf16 tiles load the next tile in a tile's last steps), 4 (they do not), 1 and a half.
+
+    Exact: a row's largest weight is 448 and times 4 is 1792 < 2^11, so the 8-bit unit's cut at 2^-13 of the largest product
+    leaves whole numbers whole; sums stay below 1792 + 832 * 16 < 2^24.  A bf16 output is their rounding.  Each expert's rows
+    are also spmm24_f8's, bit for bit."""
+    need_gpu()
+    if tile:
+        monkeypatch.setenv("P24_F8_TILE", tile)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    whole = lambda low, high, *shape: torch.randint(low, high, shape, generator=g, device="cuda").float()  # noqa: E731
+    for E, M, K, most in ((60, 1100, 832, 600), (30, 520, 448, 400), (7, 300, 192, 200), (3, 65, 64, 70)):
+        counts = torch.randint(0, most + 1, (E,), generator=torch.Generator().manual_seed(K)).tolist()
+        counts[0], counts[1], counts[-1] = 0, 257, 1
+        offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).int()
+        ends = offsets.tolist()
+        W = whole(-4, 5, E, M, K)
+        W.view(E, M, K // 4, 4)[..., 1::2] = 0              # two of every four
+        W[:, :, 0] = 448
+        ws = torch.exp2(whole(-6, 3, E, M))
+        c = p24.compress_f8_experts(W * ws[:, :, None])
+        assert torch.equal(c.scale, ws)
+        for x_rows in (ends[-1], 77):
+            q, xs = whole(-4, 5, x_rows, K), torch.exp2(whole(-4, 5, x_rows))
+            x = p24.Quantized8(q.to(torch.float8_e4m3fn), xs)
+            tokens = None if x_rows == ends[-1] else torch.randint(0, x_rows, (ends[-1],), generator=g, device="cuda", dtype=torch.int32)
+            y = p24.spmm24_f8_grouped(c, x, offsets, tokens=tokens, out_dtype=out)
+            n = p24.lib().prune24_f8_bytes(M, K)
+            for e in range(E):
+                a, b = ends[e], ends[e + 1]
+                if a == b:
+                    continue
+                src = slice(a, b) if tokens is None else tokens[a:b].long()
+                want = (q[src].double() @ W[e].double().T) * xs[src].double()[:, None] * ws[e].double()
+                assert torch.equal(y[a:b], want.float().to(out)), (E, e)
+                if e % 10 == 1:
+                    one = p24.Compressed24F8(c.data[e * n:(e + 1) * n], c.scale[e], M, K)
+                    rows = p24.Quantized8(x.values[src].contiguous(), xs[src].contiguous())
+                    assert torch.equal(y[a:b], p24.spmm24_f8(one, rows, out_dtype=out)), (E, e)
