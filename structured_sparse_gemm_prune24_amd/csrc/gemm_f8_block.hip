@@ -8,7 +8,7 @@
 // a lane's four values share one token, and a wave's rows one block of weights, so that the scale is
 // one number a lane for each 16 tokens and step.
 //
-// Bound by the matrix unit and the power it takes: 8192^3 in 435 to 474 us, 778 k cycles of which it is busy for 524 k
+// Bound by the matrix unit and the power it takes: 8192^3 in 427 to 474 us, 778 k cycles of which it is busy for 524 k
 // (675 k without loads, fragment reads and epilogue; 705 k without scaling and epilogue).
 //
 // Operands: lane L takes row (token) L % 16 and 32 of the block's k, two chunks of 16 B.  Which k a lane holds is
@@ -572,14 +572,18 @@ static p24_status launch_block_tile(F8BArgs a, hipStream_t st) {
   return launch_status();
 }
 
-// Which kernel: that of the fewest microseconds (p24_f8_cost.hpp).  Over 120 shapes drawn at random the choice is 2 %
-// behind the fastest, for both outputs (geometric mean).  Measured, us, M x K with N tokens (bf16; fp32):
-//   8192 x 8192, 8192    256x256 435, 256x128 500, 128x128 541; 128x128 889
-//   8192 x 4096, 4096    256x256 117, 256x128 133, 128x128 146; 128x128 240, 128x64 287
-//   4096 x 11264, 2048   256x128 86, 128x128 94, 256x256 125
-//   4096 x 4096, 512     128x64 15.7, 64x64 16.5, 64x32 19.0
-//   1000 x 4048, 517     64x64 11.6, 64x32 14.0; 64x64 17.3, 128x64 22.7
-//   4096 x 4096, 32      tokens 8.6, 64x32 9.1;  1 token 5.1, 8.9
+// Which kernel: that of the fewest microseconds by forecast (p24_f8_cost.hpp).  Over 80 shapes drawn at random
+// (1 to 8192 tokens and features, K 16 to 8192) it is 3.8 % behind the fastest, fp32 outputs 2.8 % (geometric means), at
+// the median 1.8 and 0.9 %, a tenth of the shapes 11 and 6 %, the worst 54 % (88 tokens, 2965 x 3184: tokens 12.7,
+// 64x32 8.2) and 36 %.  The forecast is smooth in rounds of 256 blocks, and so too low where a round has just begun.
+// Measured, us, M x K with N tokens (bf16; fp32), * the one that is taken:
+//   8192 x 8192, 8192    256x256 432*, 256x128 495, 128x128 544; 128x128 907*, 128x64 1090
+//   8192 x 4096, 4096    256x256 114*, 256x128 133, 128x128 144; 128x128 240*, 128x64 289
+//   4096 x 11264, 2048   256x128 85*, 128x128 92, 256x256 115; 128x128 160*, 128x64 193
+//   4096 x 4096, 512     128x64 15.4*, 64x64 16.0, 64x32 19.0; 128x64 22.5*, 64x64 26.3
+//   2304 x 768, 4096     256x256 14.3, 128x64 17.4, 128x128 17.6*, 64x64 18.0; 128x128 24.0*, 128x64 24.1
+//   1000 x 4048, 517     64x64 11.0, 64x32 14.1*, 128x64 18.6; 64x64 16.4, 64x32 16.6*, 128x64 22.1
+//   4096 x 4096, 32      tokens 8.1*, 64x32 8.8;  1 token 4.7*, 8.7
 enum F8BKernel { B_TOKENS, B_64x32, B_64x64, B_128x64, B_128x128, B_256x128, B_256x256, B_KERNELS };
 
 constexpr TileCost BLOCK_BF16[B_KERNELS] = {

@@ -118,20 +118,21 @@ static p24_status launch_tile_grouped(F8GroupedArgs g, hipStream_t st) {
 
 // Which kernel.  Where the rows lie is not known here: the experts' numbers of rows are taken as
 // exponentially distributed, so that an expert with a rows on average has 1 / (1 - exp(-BN / a)) tiles of BN rows.
-// With that many blocks the kernel of the fewest microseconds wins (p24_f8_cost.hpp).  Over 79 shapes of 256 to 32768
-// rows drawn at random it is 2.4 % behind the fastest, over 60 large ones (256 to 8192 tokens, 512 to 4096 k) 3.6 %
-// (fp32 outputs: 2.9 % over 160 shapes, 2.6 %; geometric means).
-// Measured, us (T tokens of k experts, of E with M x K):
-//   4096 of 8, 64 of 4096 x 2048   256x256 232, 256x192 250, 256x128 273, 128x128 316, 64x64 512
-//   2048 of 8, 128 of 2048 x 2048  256x256 103, 256x128 110, 128x128 115, 256x192 120, 64x64 168
-//   512 of 2, 8 of 4096 x 4096     256x128 23.3, 256x192 26.5, 128x128 28.3, 64x32 38.7
-//   1571 of 2, 7 of 1000 x 1088    128x128 11.1, 128x64 11.6, 64x64 13.5; fp32 15.6, 16.3, 18.0
-//   64 of 4, 32 of 4096 x 4096     64x32 59, 128x64 59, 64x64 64, tokens 73
-//   1 of 8, 128 of 2048 x 4096     tokens 9.1, 64x32 13.6
+// With that many blocks the kernel of the fewest microseconds by forecast wins (p24_f8_cost.hpp).  Over 60 shapes drawn
+// at random (1 to 8192 tokens of 2 to 128 experts) it is 3.1 % behind the fastest, fp32 outputs 1.7 % (geometric means), a
+// tenth of the shapes 8 and 4 %, the worst 21 % for both.
+// Measured, us (T tokens of k experts, of E with M x K; bf16 unless said), * the one that is taken:
+//   4096 of 8, 64 of 4096 x 2048   256x256 227*, 256x192 247, 256x128 273, 128x128 317, 64x64 499
+//   2048 of 8, 128 of 2048 x 2048  256x256 104*, 256x128 109, 128x128 113, 256x192 121, 64x64 162
+//   512 of 2, 8 of 4096 x 4096     256x128 23.4, 256x192 26.2, 128x128 28.0*, 64x32 38.4; fp32 256x128 38.5, 128x128 41.7*
+//   1571 of 2, 7 of 1000 x 1088    128x128 10.1, 128x64 10.6*, 64x64 12.4; fp32 128x128 14.1*, 128x64 14.7, 64x64 16.4
+//   64 of 4, 32 of 4096 x 4096     128x64 58.5, 64x32 59.6*, 64x64 63.7, tokens 72; fp32 64x32 63.1*, 128x64 63.0
+//   1 of 8, 128 of 2048 x 4096     tokens 8.4*, 64x64 12.8, 64x32 13.1
 //
-// What bounds the largest (measured inside the kernel, 256x256 of the first line): a tile takes 21.5 us, 15 of them its 16
-// steps, 4.4 its epilogue, 1.8 the start of the next.  A step takes as long without the multiplies (0.85 us for its 52 KB
-// a CU, 0.65 without the loads): the way from the L2 to LDS is the bound, hits or not (0.9 with every weight there).
+// What bounds the largest (measured inside the kernel, 256x256 of the first line): a tile takes 21.5 us, 15 of them its
+// 16 steps, 4.4 its epilogue, 1.8 the start of the next.  A step of 0.94 us takes 0.85 without the multiplies, 0.65
+// without the loads, 0.86 with half of its rows dead and 0.89 with every weight in the L2: its bytes and its hits do not
+// set it, which leaves the loads' latency, two steps of them in flight and one barrier a step.
 enum F8GroupedKernel { G_TOKENS, G_64x32, G_64x64, G_128x64, G_128x128, G_256x128, G_256x192, G_256x256, G_KERNELS };
 
 constexpr TileCost GROUPED_BF16[G_KERNELS] = {

@@ -9,7 +9,8 @@ namespace p24 {
 // first loads and epilogue, and a step's waits.  With many blocks a round of 256 takes many + many_step * steps: the CUs'
 // throughput, several blocks to a CU where they fit.  The time is the larger of the two, joined smoothly.  The four numbers
 // of a kernel are a least-squares fit (of the logarithm) to its times over shapes drawn at random; a
-// forecast is 10-15 % off, and what it is for is the order of the kernels.
+// forecast is 10-15 % off, up to 30 % at a shape (the rules' comments have measured ones): it is for the order of the
+// kernels.
 struct TileCost {
   int bm, bn;
   double alone, alone_step, many, many_step;

@@ -28,7 +28,8 @@ _SCORES = {"softmax": P24_SCORE_SOFTMAX, "sigmoid": P24_SCORE_SIGMOID}
 
 @dataclass
 class Routing:
-    """Which experts the tokens go to, and the rows that this makes."""
+    """Which experts the tokens go to, and the rows that this makes.  The tensors are parts of one allocation, which
+    any of them keeps (from 65 tokens on with 4 bytes of scratch an expert for every 32 tokens)."""
     experts: object      # torch.int32 [tokens, k]: best first, -1 where no expert is open
     weights: object      # torch.float32 [tokens, k]
     offsets: object      # torch.int32 [E + 1]: expert e's rows are offsets[e] to offsets[e + 1]
@@ -77,7 +78,8 @@ def route(logits, k: int, score="softmax", bias=None, normalize=True, scale=1.0)
     logits [tokens, E] fp32 or bf16; -inf closes an expert to a token (a row of -inf: a padded token).
     score "softmax" ranks by the logit and weighs by the softmax over the chosen experts (`normalize`)
     or over all; "sigmoid" ranks by sigmoid(logit) + bias (bias fp32 [E] or None) and weighs by the
-    sigmoids, over their sum with `normalize`.  Ties go to the lower expert.  Weights times `scale`."""
+    sigmoids, over their sum with `normalize` (NaN where the largest logit lies below -709.78: -inf closes
+    experts, a type's lowest value does not).  Ties go to the lower expert.  Weights times `scale`."""
     code = _SCORES.get(score)
     if code is not None and (bias is None or code == P24_SCORE_SIGMOID) and math.isfinite(scale):
         got = (_CALL or _fast()).route(logits, k, code, bias, 1 if normalize else 0, scale)
